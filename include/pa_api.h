@@ -83,6 +83,9 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2 } pa_dtype;
                                       append) not the slot of position context_len - 1 */
 #define PA_DEVERR_PREFIX 0x8u      /* pa_decode_shared_prefix: a sequence does not start
                                       with the shared prefix blocks, or is shorter */
+#define PA_DEVERR_CHUNK 0x20u    /* pa_attend_chunk, pa_gather_kv, pa_verify_draft: row starts
+                                      that run backwards, leave the rows given or exceed the
+                                      stated maximum */
 #define PA_DEVERR_TIMEOUT 0x10u    /* a kernel's bounded wait for its own tensor-core
                                       work gave up (1 s); its results are not written */
 
@@ -346,6 +349,54 @@ pa_status pa_decode_static_workspace(const void* q, int32_t q_dtype, int32_t bat
                                      const int32_t* context_lens, int32_t max_context,
                                      float scale, void* out, int32_t partition_tokens,
                                      void* stream);
+
+/* Workspace bytes for pa_attend_chunk (0 when one partition covers every
+ * context). Pure host function. */
+size_t pa_attend_chunk_workspace_size(int64_t num_tokens, int32_t batch, int32_t num_q_heads,
+                                      int32_t max_chunk, int32_t max_context, int32_t window,
+                                      int32_t partition_tokens, const pa_cache_desc* cache);
+
+/* Attention of chunks of new tokens over the paged cache: a prompt, or a
+ * part of one, or the drafted tokens of a speculative step, several
+ * sequences in one call. Sequence b brings the rows cu_chunk[b] ..
+ * cu_chunk[b + 1] of q; its new token i (of n_b) sits at position
+ * p = context_lens[b] - n_b + i and attends the sequence's cached tokens
+ * 0 .. p, its own included (with window > 0 only the last `window` of them:
+ * p - window + 1 .. p):
+ *   out[row][h][:] = softmax_j(scale * q[row][h] . K_j) V_j,  KV head h / group.
+ * The K/V of the new tokens are in the cache already (pa_append_kv, with the
+ * same cache and stream, before this call). With one new token per sequence
+ * this is pa_decode; a mixed batch (some sequences decoding one token, some
+ * running a prompt chunk, some bringing none) is one call.
+ *   q, out        [num_tokens][num_q_heads][head_dim] in q_dtype (for a
+ *                 16-bit cache, its dtype). Rows outside cu_chunk[0] ..
+ *                 cu_chunk[batch] (padding) are left as they were.
+ *   cu_chunk      [batch + 1] int32, not decreasing, within [0, num_tokens].
+ *   max_chunk     host-side upper bound of the n_b (sizes the launch).
+ *   block_tables, context_lens, max_context, scale: as for pa_decode;
+ *                 context_lens[b] includes the n_b new tokens. Table entries
+ *                 of blocks behind the sequence's last token, or holding only
+ *                 tokens before the first row's window, are not read.
+ *   window        0 (the whole history) or the tokens a row attends.
+ *   partition_tokens  0 lets the library split long contexts; otherwise a
+ *                 multiple of 128 in [128, 1 << 20].
+ *   workspace     pa_attend_chunk_workspace_size(...) bytes, 256-byte aligned.
+ * A chunk outside its rows or longer than max_chunk sets PA_DEVERR_CHUNK and
+ * is skipped; a length shorter than the chunk, above max_context or beyond
+ * the table sets PA_DEVERR_CONTEXT_LEN and gives zero rows; a bad block id
+ * sets PA_DEVERR_BLOCK_ID and its tokens read as zeros.
+ * K/V outside a row's tokens never reach it, whatever bits they hold, except
+ * that the V of a sequence's own new tokens (and of tokens the window drops
+ * within one chunk) must be finite for the rows that do not see them.
+ * Results are reproducible: the same inputs, sizes and partition length give
+ * the same bits, and any partition length agrees up to rounding. */
+pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, int32_t batch,
+                          int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                          const pa_cache_desc* cache, const int32_t* cu_chunk, int32_t max_chunk,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* context_lens, int32_t max_context, int32_t window,
+                          float scale, void* out, int32_t partition_tokens, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /* Context parallelism, part 1: pa_decode over the tokens each sequence's
  * table lists, stopping short of the final normalisation across calls, so

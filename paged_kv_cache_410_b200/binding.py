@@ -23,7 +23,7 @@ PA_OK = 0
 STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_CUDA",
           4: "PA_ERR_WORKSPACE", 5: "PA_ERR_DEVICE_BOUNDS"}
 DEVERR_BLOCK_ID, DEVERR_CONTEXT_LEN, DEVERR_SLOT, DEVERR_PREFIX = 0x1, 0x2, 0x4, 0x8
-DEVERR_TIMEOUT = 0x10
+DEVERR_TIMEOUT, DEVERR_CHUNK = 0x10, 0x20
 
 # names of every symbol include/pa_api.h declares
 EXPORTED = ["pa_append_kv", "pa_decode_workspace_size", "pa_decode_partition_tokens",
@@ -34,7 +34,8 @@ EXPORTED = ["pa_append_kv", "pa_decode_workspace_size", "pa_decode_partition_tok
             "pa_append_decode", "pa_copy_blocks_layers",
             "pa_decode_shared_prefix_partition_tokens", "pa_testing_withhold_prefix_scores",
             "pa_set_deterministic", "pa_testing_withhold_steal_counts",
-            "pa_decode_partial", "pa_merge_partials"]
+            "pa_decode_partial", "pa_merge_partials", "pa_attend_chunk_workspace_size",
+            "pa_attend_chunk"]
 
 
 class PagedAttentionError(RuntimeError):
@@ -114,6 +115,11 @@ def load_library(path: str = LIB_PATH):
     lib.pa_decode_shared_prefix_partition_tokens.restype = i32
     lib.pa_testing_withhold_prefix_scores.argtypes = [i32]
     lib.pa_testing_withhold_prefix_scores.restype = None
+    lib.pa_attend_chunk_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i32, D]
+    lib.pa_attend_chunk_workspace_size.restype = ctypes.c_size_t
+    lib.pa_attend_chunk.argtypes = [P, i32, i64, i32, i32, P, P, D, P, i32, P, i32, P, i32, i32,
+                                    ctypes.c_float, P, i32, P, ctypes.c_size_t, P]
+    lib.pa_attend_chunk.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -405,6 +411,44 @@ def pa_decode_static_workspace(q, k_cache, v_cache, block_tables, context_lens, 
                                         int(max_context), float(scale), po,
                                         int(partition_tokens), _stream(stream))
     _check(rc, "pa_decode_static_workspace")
+
+
+def pa_attend_chunk_workspace_size(num_tokens, batch, num_q_heads, max_chunk, max_context,
+                                   cache: PagedCache, window=0, partition_tokens=0) -> int:
+    lib = load_library()
+    d = cache.desc()
+    return int(lib.pa_attend_chunk_workspace_size(num_tokens, batch, num_q_heads, max_chunk,
+                                                  max_context, window, partition_tokens,
+                                                  ctypes.byref(d)))
+
+
+def pa_attend_chunk(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, scale, out,
+                    cache: PagedCache, max_chunk: int, max_context: int, window: int = 0,
+                    partition_tokens: int = 0, workspace=None, stream=None):
+    """Attention of ragged chunks of new tokens (their K/V already in the
+    cache): rows cu_chunk[b] .. cu_chunk[b + 1] of q [T, Hq, D] are the last
+    tokens of sequence b (context_lens[b] counts them), each attending the
+    cached tokens up to its own position, or the last `window` of them.
+    cu_chunk: [batch + 1] int32; rows outside it stay as they were."""
+    lib = load_library()
+    d = cache.desc()
+    if q.dim() != 3:
+        raise ValueError("q: expected [num_tokens, num_q_heads, head_dim]")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables: expected [batch, max_blocks_per_seq]")
+    batch, hq = block_tables.shape[0], q.shape[1]
+    pq = _dev(q, "q", _IO, (q.shape[0], hq, cache.head_dim))
+    pt = _dev(block_tables, "block_tables", (torch.int32,))
+    pl = _dev(context_lens, "context_lens", (torch.int32,), (batch,))
+    pc = _dev(cu_chunk, "cu_chunk", (torch.int32,), (batch + 1,))
+    po = _dev(out, "out", (q.dtype,), tuple(q.shape))
+    kc, vc = cache.cache_ptrs(k_cache, v_cache)
+    rc = lib.pa_attend_chunk(pq, _dtype_code(q.dtype), q.shape[0], batch, hq, kc, vc,
+                             ctypes.byref(d), pc, int(max_chunk), pt, block_tables.shape[1], pl,
+                             int(max_context), int(window), float(scale), po,
+                             int(partition_tokens), _dev(workspace, "workspace"),
+                             _nbytes(workspace), _stream(stream))
+    _check(rc, "pa_attend_chunk")
 
 
 def pa_copy_blocks(pairs, k_cache, v_cache, cache: PagedCache, stream=None):

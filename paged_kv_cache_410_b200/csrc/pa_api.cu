@@ -20,6 +20,7 @@
 
 #include "pa_api.h"
 #include "pa_append_copy.cuh"
+#include "pa_chunk.cuh"
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
 #include "pa_prefix.cuh"
@@ -780,6 +781,127 @@ pa_status launch_cascade_d(const pa::DecodeParams& p, const CascadePlan& pl,
   }
 }
 
+// ---- chunk attention ----------------------------------------------------------
+// Rows (token, query head) of one KV head go into row tiles of 128. Chunks
+// that fit one tile per KV head (drafts) take one-tile CTAs, two per SM, and
+// steps of 64 tokens: each reads its tokens once and is bound by HBM. Longer
+// chunks take two tiles per CTA and steps of 128 tokens, so that every K/V
+// step serves 256 rows and one tile's softmax runs beside the other's MMAs.
+struct ChunkPlan {
+  int head_rows, head_blocks, tile_tokens;
+  int tiles_per_cta, step;
+  int num_tiles;
+  int partition_tokens, num_partitions;
+  size_t ws_o_bytes, ws_bytes;
+  bool fits;
+};
+
+ChunkPlan make_chunk_plan(int64_t num_tokens, int64_t batch, int64_t num_q_heads,
+                          int64_t max_chunk, int64_t max_context, int64_t window,
+                          int partition_tokens, const pa_cache_desc* cd) {
+  ChunkPlan pl{};
+  const int64_t group = num_q_heads / cd->num_kv_heads;
+  pl.head_rows = static_cast<int>(std::min<int64_t>(group, pa::kUmmaRows));
+  pl.head_blocks = static_cast<int>((group + pl.head_rows - 1) / pl.head_rows);
+  pl.tile_tokens = pa::kUmmaRows / pl.head_rows;
+  pl.tiles_per_cta = max_chunk > pl.tile_tokens ? 2 : 1;
+  pl.step = pl.tiles_per_cta == 2 ? 128 : 64;
+  const int64_t t = static_cast<int64_t>(pl.tiles_per_cta) * pl.tile_tokens;
+  const int64_t tiles = num_tokens / t + batch;  // chunk_tile's bound
+  pl.num_tiles = static_cast<int>(tiles);
+  // tokens a CTA tile can attend, from its first (rounded) token
+  int64_t span = std::max<int64_t>(max_context, 1);
+  if (window > 0) span = std::min<int64_t>(span, window + t + pl.step);
+  const int64_t heads = static_cast<int64_t>(cd->num_kv_heads) * pl.head_blocks;
+  // CTAs with rows, when every chunk is as long as it can be
+  const int64_t units =
+      std::min<int64_t>(tiles, batch * ((max_chunk + t - 1) / t)) * heads;
+  int64_t pt = partition_tokens;
+  if (pt == 0) {
+    const int64_t slots = (pl.tiles_per_cta == 2 ? 1 : 2) * kNumSMs;
+    const int64_t want = units >= slots ? 1 : (2 * slots + units - 1) / units;
+    pt = std::max<int64_t>((span + want - 1) / want, 256);
+    pt = (pt + 127) / 128 * 128;
+  }
+  pt = std::min<int64_t>(pt, (span + 127) / 128 * 128);
+  pl.partition_tokens = static_cast<int>(pt);
+  pl.num_partitions = static_cast<int>((span + pt - 1) / pt);
+  pl.fits = tiles < (int64_t{1} << 31) &&
+            workspace_fits(num_tokens * num_q_heads, pl.num_partitions, cd->head_dim) &&
+            tiles * heads * pl.num_partitions < (int64_t{1} << 31);
+  if (pl.num_partitions > 1 && pl.fits) {
+    const size_t rows = static_cast<size_t>(num_tokens) * num_q_heads;
+    pl.ws_o_bytes = round_up(rows * pl.num_partitions * cd->head_dim * sizeof(float), 256);
+    pl.ws_bytes = pl.ws_o_bytes + round_up(rows * pl.num_partitions * sizeof(float2), 256);
+  }
+  return pl;
+}
+
+template <typename TQ, int D, int NT, int BN, int MODE>
+pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, cudaStream_t st) {
+  using C = pa::ChunkCfg<D, NT, BN, MODE>;
+  auto kern = pa::pa_chunk_kernel<TQ, D, NT, BN, MODE>;
+  if (ensure_smem(reinterpret_cast<const void*>(kern), C::kRequest) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const int64_t ctas = static_cast<int64_t>(p.num_tiles) * p.num_kv_heads * p.head_blocks *
+                       p.num_partitions;
+  kern<<<static_cast<unsigned>(ctas), C::kThreads, C::kRequest, st>>>(p, tq, tk, tv);
+  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+  if (p.num_partitions == 1) return PA_OK;
+  const int64_t rows = static_cast<int64_t>(NT) * p.tile_tokens * p.num_q_heads;
+  if ((rows + 7) / 8 > 65535) return PA_ERR_UNSUPPORTED;
+  return launch_dependent(pa::pa_chunk_merge_kernel<TQ, D>,
+                          dim3(p.num_tiles, static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,
+                          st, p, NT * p.tile_tokens, BN) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+template <typename TQ, int D, int MODE>
+pa_status launch_chunk_m(const pa::ChunkParams& p, const ChunkPlan& pl, cudaStream_t st) {
+  CUtensorMap tq{}, tk{}, tv{};
+  constexpr bool kBF16 = std::is_same<TQ, __nv_bfloat16>::value;
+  const uint64_t row = static_cast<uint64_t>(D) * 2;
+  // q [token][Hq][D]: boxes of 64 channels x a tile's query heads x its tokens
+  if (MODE != pa::kChunkE4m3 &&
+      !make_map_3d(&tq, kBF16, p.q,
+                   {static_cast<uint64_t>(D), static_cast<uint64_t>(p.num_q_heads),
+                    static_cast<uint64_t>(p.num_tokens)},
+                   {row, row * p.num_q_heads},
+                   {64u, static_cast<uint32_t>(p.head_rows), static_cast<uint32_t>(p.tile_tokens)}))
+    return PA_ERR_CUDA;
+  if (MODE == pa::kChunkTma) {
+    // caches [slot][Hkv][D]: 64 channels x 1 head x the tokens of a block (or step)
+    const uint32_t unit = static_cast<uint32_t>(std::min(1 << p.bs_log2, pl.step));
+    const uint64_t heads = static_cast<uint64_t>(p.num_kv_heads);
+    const uint64_t slots = static_cast<uint64_t>(p.num_slots);
+    if (!make_map_3d(&tk, kBF16, p.k_cache, {static_cast<uint64_t>(D), heads, slots},
+                     {row, row * heads}, {64u, 1u, unit}) ||
+        !make_map_3d(&tv, kBF16, p.v_cache, {static_cast<uint64_t>(D), heads, slots},
+                     {row, row * heads}, {64u, 1u, unit}))
+      return PA_ERR_CUDA;
+  }
+  return pl.tiles_per_cta == 2 ? launch_chunk_t<TQ, D, 2, 128, MODE>(p, tq, tk, tv, st)
+                               : launch_chunk_t<TQ, D, 1, 64, MODE>(p, tq, tk, tv, st);
+}
+
+template <typename TQ>
+pa_status launch_chunk(const pa::ChunkParams& p, const ChunkPlan& pl, const pa_cache_desc* cd,
+                       cudaStream_t st) {
+  // TMA boxes hold whole 8-token swizzle atoms and 32-bit slot coordinates
+  const bool tma = cd->block_size >= 8 &&
+                   cd->num_blocks * cd->block_size < (int64_t{1} << 31) - 1;
+  if (cd->cache_dtype == PA_E4M3)
+    return cd->head_dim == 64 ? launch_chunk_m<TQ, 64, pa::kChunkE4m3>(p, pl, st)
+                              : launch_chunk_m<TQ, 128, pa::kChunkE4m3>(p, pl, st);
+  if (tma)
+    return cd->head_dim == 64 ? launch_chunk_m<TQ, 64, pa::kChunkTma>(p, pl, st)
+                              : launch_chunk_m<TQ, 128, pa::kChunkTma>(p, pl, st);
+  return cd->head_dim == 64 ? launch_chunk_m<TQ, 64, pa::kChunkCopy>(p, pl, st)
+                            : launch_chunk_m<TQ, 128, pa::kChunkCopy>(p, pl, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -827,6 +949,89 @@ pa_status pa_decode_partial(const void* q, int32_t q_dtype, int32_t batch, int32
   p.cp_o = part_o;
   p.cp_ml = reinterpret_cast<float2*>(part_ml);
   return launch_decode(p, q_dtype, cache, as_stream(stream));
+}
+
+size_t pa_attend_chunk_workspace_size(int64_t num_tokens, int32_t batch, int32_t num_q_heads,
+                                      int32_t max_chunk, int32_t max_context, int32_t window,
+                                      int32_t partition_tokens, const pa_cache_desc* cache) {
+  int bs_log2 = 0;
+  if (check_cache(cache, &bs_log2) != PA_OK || num_tokens <= 0 || num_tokens > 0x7fffffffLL ||
+      batch <= 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 ||
+      max_chunk <= 0 || max_context < 0 || window < 0 || partition_tokens < 0)
+    return 0;
+  return make_chunk_plan(num_tokens, batch, num_q_heads, std::min<int64_t>(max_chunk, num_tokens),
+                         max_context, window, partition_tokens, cache)
+      .ws_bytes;
+}
+
+pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, int32_t batch,
+                          int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                          const pa_cache_desc* cache, const int32_t* cu_chunk, int32_t max_chunk,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* context_lens, int32_t max_context, int32_t window,
+                          float scale, void* out, int32_t partition_tokens, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (num_tokens < 0 || max_chunk < 0 || window < 0) return PA_ERR_INVALID_ARG;
+  if (partition_tokens != 0 && (partition_tokens < 128 || partition_tokens > (1 << 20) ||
+                                partition_tokens % 128 != 0))
+    return PA_ERR_INVALID_ARG;
+  int bs_log2 = 0;
+  bool nothing = false;
+  // (no rows: the checks that need none of the pointers)
+  pa_status st = check_decode_args(q, q_dtype, num_tokens == 0 || max_chunk == 0 ? 0 : batch,
+                                   num_q_heads, k_cache, v_cache, cache, block_tables,
+                                   max_blocks_per_seq, context_lens, max_context, scale, out, 0,
+                                   &bs_log2, &nothing);
+  if (st != PA_OK) return st;
+  if (batch < 0) return PA_ERR_INVALID_ARG;
+  if (nothing) return PA_OK;
+  if (!cu_chunk) return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+  max_chunk = static_cast<int32_t>(std::min<int64_t>(max_chunk, num_tokens));
+  const ChunkPlan pl = make_chunk_plan(num_tokens, batch, num_q_heads, max_chunk, max_context,
+                                       window, partition_tokens, cache);
+  if (!pl.fits) return PA_ERR_UNSUPPORTED;
+  if (pl.ws_bytes > 0) {
+    if (!workspace || workspace_bytes < pl.ws_bytes) return PA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_WORKSPACE;
+  }
+  pa::ChunkParams p{};
+  p.q = q;
+  p.out = out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.cu = cu_chunk;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  if (pl.ws_bytes > 0) {
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + pl.ws_o_bytes);
+  }
+  p.num_blocks = cache->num_blocks;
+  p.num_tokens = num_tokens;
+  p.batch = batch;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.group = num_q_heads / cache->num_kv_heads;
+  p.head_rows = pl.head_rows;
+  p.head_blocks = pl.head_blocks;
+  p.tile_tokens = pl.tile_tokens;
+  p.num_tiles = pl.num_tiles;
+  p.num_partitions = pl.num_partitions;
+  p.partition_tokens = pl.partition_tokens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.bs_log2 = bs_log2;
+  p.max_chunk = max_chunk;
+  p.max_context = max_context;
+  p.window = window;
+  p.num_slots = static_cast<int>(
+      std::min<int64_t>(cache->num_blocks * cache->block_size, 0x7fffffff));
+  p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * 1.4426950408889634f;
+  p.sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+  return q_dtype == PA_F16 ? launch_chunk<__half>(p, pl, cache, as_stream(stream))
+                           : launch_chunk<__nv_bfloat16>(p, pl, cache, as_stream(stream));
 }
 
 pa_status pa_merge_partials(const float* part_o, const float* part_ml, int32_t num_parts,

@@ -1,0 +1,804 @@
+// Attention of chunks of new tokens over the paged cache (sm_100a).
+//
+// Sequence b brings n_b new tokens (rows cu[b] .. cu[b+1] of q), whose K/V
+// the caller has already stored; the row of new token i sits at position
+// p = L_b - n_b + i and attends the cached tokens max(0, p - w + 1) .. p
+// (w = the window, unlimited without one):
+//   out = sum_j 2^(s_j - m) V_j / sum_j 2^(s_j - m),  s_j = scale log2(e) q.K_j.
+//
+// For one KV head the rows (token, query head of the group) of a run of new
+// tokens against the cached tokens are a dense problem, so a CTA takes NT
+// tiles of up to 128 such rows and walks the tokens in steps of BN:
+//   S (128 x BN, f32, TMEM)     = Q (128 x D, smem) . K_step^T (BN x D, smem)
+//   P (128 x BN, 16-bit, TMEM)  = 2^(S - m), over S's own columns
+//   O (128 x D, f32, TMEM)     += P (TMEM) . V_step (BN x D, smem)
+// with the running maximum m and sum l of a row in the registers of the one
+// thread that owns the row. K and V steps come through one ring of NBUF
+// buffers (K0 V0 K1 V1 ...), filled by one TMA warp (16-bit caches with
+// blocks of 8 tokens or more: whole 1024-byte swizzle atoms per box), or by
+// four loader warps with cp.async (smaller blocks; E4M3 caches, which they
+// widen to f16: exact).
+//
+// What each row may not see is decided by selecting on S, so K of masked
+// tokens never matters; V rows outside the CTA's token range (behind the
+// last row's position, before the first row's window: recycled memory) are
+// zeroed in shared memory, since 0 x NaN would reach the sum.
+#pragma once
+
+#include "pa_prefix_umma.cuh"
+
+namespace pa {
+
+struct ChunkParams {
+  const void* q;              // [num_tokens][Hq][D]
+  void* out;                  // [num_tokens][Hq][D]
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;       // E4M3 caches
+  const float* v_scale;
+  const int32_t* cu;          // [batch + 1]
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* ws_o;                // [num_tokens * Hq][num_partitions][D] (split contexts)
+  float2* ws_ml;              // [num_tokens * Hq][num_partitions]
+  int64_t num_blocks;
+  int64_t num_tokens;
+  int batch;
+  int num_q_heads;
+  int num_kv_heads;
+  int group;                  // query heads per KV head
+  int head_rows;              // query heads of a group in one row tile: min(group, 128)
+  int head_blocks;            // ceil(group / head_rows)
+  int tile_tokens;            // new tokens in one row tile: 128 / head_rows
+  int num_tiles;              // grid bound: CTA tiles over the batch
+  int num_partitions;
+  int partition_tokens;       // a multiple of the kernel's BN
+  int max_blocks_per_seq;
+  int bs_log2;
+  int max_chunk;
+  int max_context;
+  int window;                 // 0: the whole history
+  int num_slots;              // TMA: a slot past the map (loads zeros)
+  float scale_log2;           // |scale| * log2(e)
+  float sign;                 // 1, -1 or 0: the sign of scale
+};
+
+// Which new tokens a CTA tile holds, and the cached tokens they attend.
+struct ChunkTile {
+  int b;        // sequence (-1: no rows, the CTA has nothing to do)
+  int i0;       // first new token of the tile within the chunk
+  int tokens;   // new tokens in the tile
+  int64_t row;  // first row of q / out
+  int pos0;     // position of token i0
+  int lo, hi;   // cached tokens [lo, hi) any row of the tile attends
+  int base;     // lo rounded down to the step: where the partitions start
+};
+
+// Tiles are laid over the batch without reading lengths on the host: sequence
+// b owns tile indices from f(b) = cu[b] / t + b (t tokens per tile), which
+// leaves it at least ceil(n_b / t) of them; surplus tiles have no rows. One
+// warp finds b, the last sequence with f(b) <= x, 32 probes at a time.
+__device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int t, int step) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int stride = (hi - lo + 31) >> 5;
+    const int at = lo + lane * stride;
+    const bool below = at < hi && __ldg(p.cu + at) / t + at <= x;
+    const unsigned m = __ballot_sync(0xffffffffu, below);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * stride;
+    hi = min(lo + stride, hi);
+  }
+  ChunkTile c;
+  c.b = -1;
+  c.i0 = c.tokens = c.pos0 = c.lo = c.hi = c.base = 0;
+  c.row = 0;
+  const int start = __ldg(p.cu + lo);
+  const int end = __ldg(p.cu + lo + 1);
+  const int L = __ldg(p.context_lens + lo);
+  // a chunk outside [0, num_tokens) or longer than max_chunk is not touched
+  if (start < 0 || end < start || end > p.num_tokens || end - start > p.max_chunk) {
+    if (lane == 0) flag_error(PA_DEVERR_CHUNK);
+    return c;
+  }
+  const int n = end - start;
+  const int64_t first = static_cast<int64_t>(x - (start / t + lo)) * t;
+  if (first < 0 || first >= n) return c;
+  c.b = lo;
+  c.i0 = static_cast<int>(first);
+  c.tokens = min(t, n - c.i0);
+  c.row = static_cast<int64_t>(start) + c.i0;
+  // a length the table or the launch cannot hold: the rows see no tokens
+  if (L < n || L > p.max_context ||
+      L > (static_cast<int64_t>(p.max_blocks_per_seq) << p.bs_log2)) {
+    if (lane == 0) flag_error(PA_DEVERR_CONTEXT_LEN);
+    return c;
+  }
+  c.pos0 = L - n + c.i0;
+  c.hi = c.pos0 + c.tokens;
+  c.lo = p.window > 0 ? max(0, c.pos0 - p.window + 1) : 0;
+  c.base = c.lo / step * step;
+  return c;
+}
+
+// MODE: how K / V reach shared memory.
+constexpr int kChunkTma = 0;     // TMA boxes (16-bit, blocks >= 8)
+constexpr int kChunkCopy = 1;    // cp.async (16-bit, smaller blocks)
+constexpr int kChunkE4m3 = 2;    // cp.async of codes, widened to f16
+
+template <int D, int NT, int BN, int MODE>
+struct ChunkCfg {
+  static constexpr int kSoftmaxWarps = 4 * NT;
+  static constexpr int kLoadWarps = MODE == kChunkTma ? 1 : 4;
+  static constexpr int kLoadThreads = 32 * kLoadWarps;
+  static constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  // TMEM columns: S (and P) of tile t at t * BN, O of tile t behind them
+  static constexpr int kOCol = NT * BN;
+  static constexpr int kColsUsed = kOCol + NT * D;
+  static constexpr int kTmemCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
+  static_assert(kColsUsed <= 512, "TMEM holds 512 columns");
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kQTile = kSlabs * kUmmaRows * 128;
+  static constexpr int kBufSlab = BN * 128;
+  static constexpr int kBuf = kSlabs * kBufSlab;  // one K or V step, 16-bit
+  static constexpr int kRaw = MODE == kChunkE4m3 ? kBuf / 2 : 0;  // its E4M3 codes
+  static constexpr int kRawStages = MODE == kChunkE4m3 ? (NT == 1 ? 3 : 4) : 0;
+  // bytes for tiles: 224 KB for one CTA per SM, 111 KB for two
+  static constexpr int kCtas = NT == 1 ? 2 : 1;
+  static constexpr int kBudget = kCtas == 2 ? 111 * 1024 : 224 * 1024;
+  static constexpr int kFit = (kBudget - NT * kQTile - kRawStages * kRaw) / kBuf;
+  static constexpr int kBufs = kFit < 8 ? kFit : 8;
+  static_assert(kBufs >= 3, "a K and a V step in use and one arriving");
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + NT * kQTile;
+  static constexpr int kRawOff = kRing + kBufs * kBuf;
+  static constexpr int kBytes = kRawOff + kRawStages * kRaw;
+  static constexpr int kSmall = 256;  // barriers, TMEM address, abort flag
+  static constexpr int kRequest = 1024 + kBytes + kSmall;
+};
+
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Grid: tiles x KV heads x head blocks x partitions, partition fastest, the
+// batch's last tiles first (in a causal chunk they see the most tokens).
+template <typename TQ, int D, int NT, int BN, int MODE>
+__global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
+                                  ChunkCfg<D, NT, BN, MODE>::kCtas)
+    pa_chunk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v) {
+  using C = ChunkCfg<D, NT, BN, MODE>;
+  // the operands' type: an E4M3 cache is widened to f16, and q folded into it
+  constexpr bool BF16 = MODE != kChunkE4m3 && std::is_same<TQ, __nv_bfloat16>::value;
+  constexpr int SLABS = C::kSlabs;
+  constexpr int NBUF = C::kBufs;
+  constexpr uint32_t kIdescS = umma_idesc<BF16, BN, false>();
+  constexpr uint32_t kIdescPV = umma_idesc<BF16, D, true>();
+
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t raw = smem_addr(smem);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t small = base + C::kBytes;
+  const uint32_t bar_full = small;            // + 8 * buffer (<= 8)
+  const uint32_t bar_free = small + 64;       // + 8 * buffer
+  const uint32_t bar_s = small + 128;         // + 8 * tile
+  const uint32_t bar_p = small + 144;         // + 8 * tile
+  const uint32_t bar_o = small + 160;         // + 8 * tile
+  const uint32_t bar_q = small + 176;
+  const uint32_t bar_done = small + 184;
+  const uint32_t tmem_slot = small + 192;
+  const uint32_t abort = small + 196;
+  const uint32_t sQ = base + C::kQ;
+  const uint32_t sRing = base + C::kRing;
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  // one CTA looks at the whole of cu: chunks that overlap, run backwards or
+  // leave [0, num_tokens) may own no tile that would notice
+  if (blockIdx.x == 0)
+    for (int i = tid; i < p.batch; i += C::kThreads)
+      if (p.cu[i] < 0 || p.cu[i + 1] < p.cu[i] || p.cu[i + 1] > p.num_tokens)
+        flag_error(PA_DEVERR_CHUNK);
+
+  // this CTA's unit
+  int u = blockIdx.x;
+  const int part = u % p.num_partitions;
+  u /= p.num_partitions;
+  const int hb = u % p.head_blocks;
+  u /= p.head_blocks;
+  const int hk = u % p.num_kv_heads;
+  const int x = p.num_tiles - 1 - u / p.num_kv_heads;
+  const ChunkTile ct = chunk_tile(p, x, NT * p.tile_tokens, BN);
+  if (ct.b < 0) return;
+  const int h0 = hk * p.group + hb * p.head_rows;                 // first query head
+  const int heads = min(p.head_rows, p.group - hb * p.head_rows);  // query heads here
+  // this partition's tokens: steps of BN from c0
+  const int c0 = ct.base + part * p.partition_tokens;
+  const int c1 = min(c0 + p.partition_tokens, ct.hi);
+  if (c0 >= c1 && part > 0) return;  // (partition 0 writes the zeros of rows without tokens)
+  const int nsteps = c0 < c1 ? (c1 - c0 + BN - 1) / BN : 0;
+  const int ntiles = (ct.tokens + p.tile_tokens - 1) / p.tile_tokens;
+  // steps [tile_a, tile_b) that tile t's rows see any token of
+  auto tile_b = [&](int t) {
+    const int end = min(c1, ct.pos0 + min((t + 1) * p.tile_tokens, ct.tokens));
+    return end > c0 ? (end - c0 + BN - 1) / BN : 0;
+  };
+  auto tile_a = [&](int t) {
+    if (p.window <= 0) return 0;
+    const int first = ct.pos0 + t * p.tile_tokens - p.window + 1;
+    return min(first > c0 ? (first - c0) / BN : 0, tile_b(t));
+  };
+
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == C::kMmaWarp * 32) {
+    for (int i = 0; i < NBUF; ++i) {
+      mbar_init(bar_full + 8 * i, MODE == kChunkTma ? 1 : C::kLoadThreads);
+      mbar_init(bar_free + 8 * i, 1);
+    }
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(bar_s + 8 * t, 1);
+      mbar_init(bar_p + 8 * t, 128);
+      mbar_init(bar_o + 8 * t, 1);
+    }
+    mbar_init(bar_q, MODE == kChunkE4m3 ? 128 * NT : 1);
+    mbar_init(bar_done, 1);
+    asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(abort), "r"(0u) : "memory");
+    mbar_init_fence();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(tmem) : "r"(tmem_slot));
+  bool ok = true;
+  // buffer n of the ring (K of step it: n = 2 it, V: 2 it + 1)
+  auto buf = [&](int n) { return sRing + static_cast<uint32_t>(n % NBUF) * C::kBuf; };
+  auto parity = [](int n) { return static_cast<uint32_t>((n / NBUF) & 1); };
+  const int32_t* table = p.block_tables + static_cast<int64_t>(ct.b) * p.max_blocks_per_seq;
+  auto block_of = [&](int j) -> int {  // physical block of token j, -1 if out of range
+    const int id = __ldg(table + (j >> p.bs_log2));
+    if (id < 0 || id >= p.num_blocks) {
+      flag_error(PA_DEVERR_BLOCK_ID);
+      return -1;
+    }
+    return id;
+  };
+
+  // one warp loads the row tiles of q (16-bit operands: as they are; boxes of
+  // the tile's tokens x its query heads; rows of other chunks come along) and
+  // sees them land before the CTA exits
+  auto load_q = [&]() {
+    if (nsteps <= 0) return;
+    if (lane == 0) mbar_arrive_expect_tx(bar_q, ntiles * SLABS * p.tile_tokens * p.head_rows * 128);
+    __syncwarp();
+    if (lane < ntiles * SLABS) {
+      const int t = lane / SLABS;
+      const int s = lane % SLABS;
+      tma_load_3d(sQ + t * C::kQTile + s * (kUmmaRows * 128), &tm_q, bar_q, s * 64, h0,
+                  static_cast<int>(ct.row) + t * p.tile_tokens);
+    }
+  };
+  auto drain_q = [&]() {
+    if (nsteps > 0 && lane == 0) mbar_wait(bar_q, 0);
+  };
+
+  if (warp >= C::kSoftmaxWarps && warp < C::kMmaWarp) {
+    if constexpr (MODE == kChunkTma) {
+      // ---- TMA producer: lane i issues box (unit i / SLABS, slab i % SLABS) ----
+      if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+      }
+      const int bs_mask = (1 << p.bs_log2) - 1;
+      const int unit = min(1 << p.bs_log2, BN);
+      const int nbox = BN / unit * SLABS;  // <= 32
+      const int u0 = lane / SLABS * unit;
+      const int sl = lane % SLABS;
+      // slot of this lane's unit in step `it`; units without a token of
+      // [lo, hi), and bad blocks, read past the map: zeros. Their table
+      // entries are not looked up.
+      auto slot_of = [&](int it) -> int {
+        const int j = c0 + it * BN + u0;
+        if (lane >= nbox || j >= c1 || j + unit <= ct.lo) return p.num_slots;
+        const int blk = block_of(j);
+        return blk < 0 ? p.num_slots : (blk << p.bs_log2) + (j & bs_mask);
+      };
+      auto load = [&](const CUtensorMap* map, int n, int slot) {
+        const uint32_t bar = bar_full + 8 * (n % NBUF);
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kBuf);
+        __syncwarp();
+        if (lane < nbox) tma_load_3d(buf(n) + sl * C::kBufSlab + u0 * 128, map, bar, sl * 64, hk, slot);
+      };
+      load_q();
+      int issued = 0;
+      int slot = nsteps > 0 ? slot_of(0) : 0;
+      for (int it = 0; it < nsteps && ok; ++it) {
+        const int next = it + 1 < nsteps ? slot_of(it + 1) : 0;
+        for (int n = 2 * it; n < 2 * it + 2; ++n) {
+          if (n >= NBUF &&
+              !__all_sync(0xffffffffu, mbar_wait_or_abort(bar_free + 8 * (n % NBUF),
+                                                          parity(n - NBUF), abort))) {
+            ok = false;
+            break;
+          }
+          load((n & 1) ? &tm_v : &tm_k, n, slot);
+          issued = n + 1;
+        }
+        slot = next;
+      }
+      // every issued copy has landed before the CTA can exit
+      if (lane == 0) {
+        for (int n = max(issued - NBUF, 0); n < issued; ++n)
+          mbar_wait(bar_full + 8 * (n % NBUF), parity(n));
+      }
+      drain_q();
+    } else {
+      // ---- loader warps: 16-byte pieces with cp.async -------------------------
+      const int lt = tid - C::kSoftmaxWarps * 32;
+      constexpr int kElem = MODE == kChunkE4m3 ? 1 : 2;
+      constexpr int kPieces = D * kElem / 16;            // per token row
+      constexpr int kPer = BN * kPieces / C::kLoadThreads;  // per thread and step
+      static_assert(kPer * C::kLoadThreads == BN * kPieces, "whole rounds");
+      const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D * kElem;
+      const uint32_t sRaw = base + C::kRawOff;
+      // start the copies of ring buffer n (into the raw stage, or the buffer
+      // itself); tokens outside [lo, c1) and bad blocks become zeros
+      auto start = [&](int n) {
+        const char* cache = reinterpret_cast<const char*>((n & 1) ? p.v_cache : p.k_cache);
+        int64_t slot[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int j = c0 + (n >> 1) * BN + (lt + k * C::kLoadThreads) / kPieces;
+          slot[k] = -1;
+          if (j >= ct.lo && j < c1) {
+            const int blk = block_of(j);
+            if (blk >= 0)
+              slot[k] = (static_cast<int64_t>(blk) << p.bs_log2) + (j & ((1 << p.bs_log2) - 1));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int piece = lt + k * C::kLoadThreads;
+          const int r = piece / kPieces, c = piece % kPieces;
+          const char* src = slot[k] < 0 ? cache : cache + slot[k] * row_bytes + hk * (D * kElem) + c * 16;
+          uint32_t dst;
+          if constexpr (MODE == kChunkE4m3)
+            dst = sRaw + (n % C::kRawStages) * C::kRaw + piece * 16;
+          else
+            dst = buf(n) + (c >> 3) * C::kBufSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          cp_async_16(dst, src, slot[k] < 0 ? 0u : 16u);
+        }
+      };
+      // finish buffer n: its copies (this thread's own) have landed
+      auto finish = [&](int n) {
+        if constexpr (MODE == kChunkE4m3) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int piece = lt + k * C::kLoadThreads;
+            const int r = piece / kPieces, c = piece % kPieces;
+            const uint4 w = lds128(sRaw + (n % C::kRawStages) * C::kRaw + piece * 16);
+            uint4 h[2];
+            e4m3x4_to_f16x2x2(w.x, h[0].x, h[0].y);
+            e4m3x4_to_f16x2x2(w.y, h[0].z, h[0].w);
+            e4m3x4_to_f16x2x2(w.z, h[1].x, h[1].y);
+            e4m3x4_to_f16x2x2(w.w, h[1].z, h[1].w);
+            // the row's two slabs would meet in the same banks: the upper
+            // slab's threads store their odd half first
+            const bool odd = c >= 4;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int half = e ^ (odd ? 1 : 0);
+              const int cc = 2 * c + half;
+              const uint4 v = half ? h[1] : h[0];
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                               buf(n) + (cc >> 3) * C::kBufSlab + r * 128 +
+                               (((cc & 7) ^ (r & 7)) << 4)),
+                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
+            }
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(bar_full + 8 * (n % NBUF));
+      };
+      // copies run kAhead buffers ahead of their use
+      constexpr int kAhead = MODE == kChunkE4m3 ? C::kRawStages - 1 : NBUF - 2;
+      const int total = 2 * nsteps;
+      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) load_q();
+      auto wait_free = [&](int n) {
+        return n < NBUF || mbar_wait_or_abort(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
+      };
+      for (int n = 0; n < total + kAhead; ++n) {
+        if (n < total) {
+          if (MODE == kChunkCopy && !wait_free(n)) break;
+          start(n);
+        }
+        cp_async_commit();
+        const int m = n - kAhead;
+        if (m >= 0) {
+          cp_async_wait<kAhead>();
+          if (MODE == kChunkE4m3 && !wait_free(m)) break;
+          finish(m);
+        }
+      }
+      cp_async_wait<0>();
+      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) drain_q();
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ---- MMA issue --------------------------------------------------------------
+    // MMAs of one thread run in issue order, so S(it + 1) may follow the P.V(it)
+    // that reads P from the same columns, and a full S also says that the
+    // tile's earlier P.V are done.
+    if (lane == 0 && nsteps > 0) {
+      int a[NT], b[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        a[t] = t < ntiles ? tile_a(t) : 0;
+        b[t] = t < ntiles ? tile_b(t) : 0;
+      }
+      auto full = [&](int n) {
+        return mbar_wait_or_abort(bar_full + 8 * (n % NBUF), parity(n), abort);
+      };
+      auto issue_s = [&](int t, int it) {
+        const uint32_t k = buf(2 * it);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t ad = sw128_desc(
+              sQ + t * C::kQTile + (kk >> 2) * (kUmmaRows * 128) + (kk & 3) * 32, 16, 1024);
+          const uint64_t bd = sw128_desc(k + (kk >> 2) * C::kBufSlab + (kk & 3) * 32, 16, 1024);
+          umma_f16(tmem + t * BN, ad, bd, kIdescS, kk > 0);
+        }
+        umma_commit(bar_s + 8 * t);
+      };
+      ok = mbar_wait_or_abort(bar_q, 0, abort) && full(0);
+      tc_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (a[t] == 0 && b[t] > 0) issue_s(t, 0);
+        umma_commit(bar_free);
+      }
+      for (int it = 0; ok && it < nsteps; ++it) {
+        const uint32_t v = buf(2 * it + 1);
+        const bool more = it + 1 < nsteps;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (ok && it >= a[t] && it < b[t]) {
+            ok = mbar_wait_or_abort(bar_p + 8 * t, static_cast<uint32_t>((it - a[t]) & 1), abort) &&
+                 full(2 * it + 1);
+            if (ok) {
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                umma_f16_tmem_a(tmem + C::kOCol + t * D, tmem + t * BN + kk * 8,
+                                sw128_desc(v + kk * 16 * 128, C::kBufSlab, 1024), kIdescPV,
+                                (it > a[t] || kk > 0) ? 1u : 0u);
+              if (it == b[t] - 1) umma_commit(bar_o + 8 * t);
+            }
+          }
+          if (ok && more && it + 1 >= a[t] && it + 1 < b[t]) {
+            ok = full(2 * it + 2);
+            if (ok) {
+              tc_fence_after();
+              issue_s(t, it + 1);
+            }
+          }
+        }
+        if (!ok || !full(2 * it + 1)) break;
+        umma_commit(bar_free + 8 * ((2 * it + 1) % NBUF));
+        if (more) {
+          if (!full(2 * it + 2)) break;
+          umma_commit(bar_free + 8 * ((2 * it + 2) % NBUF));
+        }
+      }
+      // every issued MMA has completed before TMEM is released
+      umma_commit(bar_done);
+      mbar_wait(bar_done, 0);
+    }
+  } else {
+    // ---- softmax: thread = row ----------------------------------------------------
+    const int tile = warp >> 2;
+    const int my_row = tid & (kUmmaRows - 1);
+    const int my_tok = tile * p.tile_tokens + my_row / p.head_rows;  // within the CTA tile
+    const int my_head = my_row % p.head_rows;
+    const bool live = my_row < p.tile_tokens * p.head_rows && my_tok < ct.tokens && my_head < heads;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + t_lane + tile * BN;
+    const uint32_t tO = tmem + t_lane + C::kOCol + tile * D;
+    const int64_t row = (ct.row + my_tok) * p.num_q_heads + h0 + my_head;
+    const int pos = ct.pos0 + my_tok;
+    const int first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    float scale_log2 = p.scale_log2;
+    if constexpr (MODE == kChunkE4m3) {
+      // q' = q * k_scale in f16: each row is divided by the power of two of
+      // its largest |q * k_scale| first (and its scale multiplied by it), so
+      // that no product leaves f16's range whatever the scales
+      if (nsteps > 0) {
+        float mx = 0.f;
+        const TQ* q = reinterpret_cast<const TQ*>(p.q) + row * D;
+        const float4* ks = reinterpret_cast<const float4*>(p.k_scale + static_cast<int64_t>(hk) * D);
+        auto piece = [&](int c, float (&y)[8]) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(q) + c);
+          const TQ* e = reinterpret_cast<const TQ*>(&w);
+          const float4 s0 = __ldg(ks + 2 * c), s1 = __ldg(ks + 2 * c + 1);
+          const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = to_f32<TQ>(e[i]) * s[i];
+        };
+        if (live) {
+#pragma unroll 2
+          for (int c = 0; c < D / 8; ++c) {
+            float y[8];
+            piece(c, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(y[i]));
+          }
+        }
+        int e2 = 0;
+        if (mx > 0.f && mx < INFINITY) frexpf(mx, &e2);
+        e2 = max(-120, min(e2, 120));
+        const float down = ldexpf(1.f, -e2);
+        scale_log2 *= ldexpf(1.f, e2);
+#pragma unroll 2
+        for (int c = 0; c < D / 8; ++c) {
+          float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (live) piece(c, y);
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack2<false>(y[2 * i] * down, y[2 * i + 1] * down);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                           sQ + tile * C::kQTile + (c >> 3) * (kUmmaRows * 128) + my_row * 128 +
+                           (((c & 7) ^ (my_row & 7)) << 4)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        fence_async_smem();
+        mbar_arrive(bar_q);
+      }
+    }
+    const int a = tile < ntiles ? tile_a(tile) : 0;
+    const int b = tile < ntiles ? tile_b(tile) : 0;
+    // the first and last position of this tile's rows: steps inside what all
+    // of them see need no mask
+    const int pos_first = ct.pos0 + tile * p.tile_tokens;
+    const int pos_last = ct.pos0 + min((tile + 1) * p.tile_tokens, ct.tokens) - 1;
+    float m_run = -INFINITY;
+    float l_run = 0.f;
+    for (int it = a; it < b; ++it) {
+      const int j0 = c0 + it * BN;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_or_abort(bar_s + 8 * tile, static_cast<uint32_t>((it - a) & 1), abort));
+      if (!ok) break;
+      tc_fence_after();
+      if (warp_live) {
+        float s[BN];
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) {
+          float h[32];
+          tmem_ld32(tS + c, h);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[c + j] = h[j];
+        }
+        tmem_ld_wait();
+        if (p.sign != 1.f) {  // a negative or zero scale
+#pragma unroll
+          for (int j = 0; j < BN; ++j) s[j] *= p.sign;
+        }
+        // tokens this row does not attend
+        if (j0 + BN - 1 > pos_first || (p.window > 0 && j0 <= pos_last - p.window) || j0 + BN > c1) {
+          const int up = min(pos, c1 - 1) - j0;
+          const int dn = first - j0;
+#pragma unroll
+          for (int j = 0; j < BN; ++j)
+            if (j > up || j < dn) s[j] = -INFINITY;
+        }
+        float m8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m8[i] = s[i];
+#pragma unroll
+        for (int j = 8; j < BN; ++j) m8[j & 7] = fmaxf(m8[j & 7], s[j]);
+        float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                         fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        mx *= scale_log2;
+        const bool up = mx > m_run + kRescaleLog2;  // (the first finite maximum always moves it)
+        const float m_ref = up ? mx : m_run;
+        const float alpha = up ? ex2(m_run - m_ref) : 1.f;
+        // a row that has seen no token yet keeps p = 2^(-inf) = 0
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t sc2 = pack_f32x2(scale_log2, scale_log2);
+        const uint64_t nm2 = pack_f32x2(neg_m, neg_m);
+        uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < BN; c += 64) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) {
+            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(s[c + j], s[c + j + 1]), sc2, nm2));
+            const float p0 = ex2(y.x);
+            const float p1 = ex2(y.y);
+            sum2[(j >> 1) & 1] = add_f32x2(sum2[(j >> 1) & 1], pack_f32x2(p0, p1));
+            pw[j / 2] = pack2<BF16>(p0, p1);
+          }
+          tmem_st32u(tS + c / 2, pw);
+        }
+        const float2 t2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
+        l_run = l_run * alpha + (t2.x + t2.y);
+        m_run = m_ref;
+        // rows whose reference maximum moved rescale their O row (the tile's
+        // earlier P.V are done: S(it) was issued behind them)
+        if (it > a && __any_sync(0xffffffffu, up)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(tO + c, o);
+          }
+        }
+        tmem_st_wait();
+      }
+      if constexpr (MODE == kChunkTma) {
+        // V rows that no row of the CTA attends: zeros (their blocks may hold anything)
+        const int z_hi = max(c1 - j0, 0), z_lo = ct.lo - j0;
+        if (z_hi < BN || z_lo > 0) {
+          const int n = 2 * it + 1;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_or_abort(bar_full + 8 * (n % NBUF), parity(n), abort));
+          if (!ok) break;
+          for (int i = my_row; i < BN * SLABS * 8; i += 128) {
+            const int r = i >> 3 & (BN - 1);
+            if (r >= z_hi || r < z_lo)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(buf(n) + i * 16), "r"(0u)
+                           : "memory");
+          }
+          fence_async_smem();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar_p + 8 * tile);
+    }
+    if (ok && b > a) {
+      ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar_o + 8 * tile, 0u, abort));
+      tc_fence_after();
+    }
+    // ---- the row's result (or its partial) -------------------------------------------
+    if (ok && warp_live && tile < ntiles) {
+      const bool any = b > a;
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // no token attended: zeros
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (any) {
+          tmem_ld32(tO + c, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = any && l_run != 0.f ? o[e] * inv : 0.f;
+        if constexpr (MODE == kChunkE4m3) {
+          const float4* vs = reinterpret_cast<const float4*>(p.v_scale + static_cast<int64_t>(hk) * D + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 s = __ldg(vs + e);
+            o[4 * e] *= s.x;
+            o[4 * e + 1] *= s.y;
+            o[4 * e + 2] *= s.z;
+            o[4 * e + 3] *= s.w;
+          }
+        }
+        if (live) {
+          if (p.num_partitions > 1) {
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + (row * p.num_partitions + part) * D + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<TQ*>(p.out) + row * D + c);
+            constexpr bool kOutBf16 = std::is_same<TQ, __nv_bfloat16>::value;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack2<kOutBf16>(o[8 * e], o[8 * e + 1]),
+                                  pack2<kOutBf16>(o[8 * e + 2], o[8 * e + 3]),
+                                  pack2<kOutBf16>(o[8 * e + 4], o[8 * e + 5]),
+                                  pack2<kOutBf16>(o[8 * e + 6], o[8 * e + 7]));
+          }
+        }
+      }
+      if (live && p.num_partitions > 1)
+        p.ws_ml[row * p.num_partitions + part] = make_float2(m_run, l_run);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  uint32_t aborted;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(aborted) : "r"(abort));
+  if (aborted && tid == 0) flag_error(PA_DEVERR_TIMEOUT);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Merge of a split context: one warp per row of a CTA tile, the row's
+// partials that the attention kernel wrote (the tile's own token range says
+// how many), weighted by l 2^(m - max m).
+template <typename TQ, int D>
+__global__ void __launch_bounds__(256) pa_chunk_merge_kernel(const ChunkParams p, int cta_tokens,
+                                                             int step) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const ChunkTile ct = chunk_tile(p, blockIdx.x, cta_tokens, step);
+  if (ct.b < 0) return;
+  const int r = blockIdx.y * 8 + warp;  // row of the tile: (token, query head)
+  if (r >= ct.tokens * p.num_q_heads) return;
+  const int64_t row = ct.row * p.num_q_heads + r;
+  const int parts = max(1, (ct.hi - ct.base + p.partition_tokens - 1) / p.partition_tokens);
+  const float2* ml = p.ws_ml + row * p.num_partitions;
+  float m = -INFINITY;
+  for (int i = lane; i < parts; i += 32) {
+    const float2 v = ml[i];
+    if (v.y != 0.f) m = fmaxf(m, v.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  constexpr int V = D / 32;  // channels per lane
+  float acc[V] = {};
+  float l = 0.f;
+  const float* po = p.ws_o + row * p.num_partitions * D + lane * V;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float2 v = ml[i];
+    const float w = v.y != 0.f ? v.y * ex2(v.x - m) : 0.f;
+    l += w;
+    float o[V];
+    if constexpr (V == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * D);
+      o[0] = f.x, o[1] = f.y, o[2] = f.z, o[3] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(i) * D);
+      o[0] = f.x, o[1] = f.y;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] += w != 0.f ? w * o[e] : 0.f;
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  TQ* out = reinterpret_cast<TQ*>(p.out) + row * D + lane * V;
+  constexpr bool BF16 = std::is_same<TQ, __nv_bfloat16>::value;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+}
+
+}  // namespace pa

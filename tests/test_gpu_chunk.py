@@ -1,0 +1,241 @@
+"""Chunk attention over the paged cache (pa_attend_chunk) on the GPU, against
+float64 attention row by row (tests/chunk_plain.py, whose docstring derives
+the bound that every value is held to)."""
+import pytest
+import torch
+
+from paged_kv_cache_410_b200 import binding as B
+from chunk_plain import attend_chunk, chunk_case, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def cache_of(g):
+    sc = {}
+    if g["k"].dtype == torch.uint8:
+        sc = dict(k_scale=g["k_scale"], v_scale=g["v_scale"], k_inv_scale=1 / g["k_scale"],
+                  v_inv_scale=1 / g["v_scale"])
+    return B.PagedCache.for_tensor(g["k"], **sc)
+
+
+def call(g, window=0, partition_tokens=0, scale=None, stream=None, out=None, workspace="own"):
+    cache = cache_of(g)
+    need = B.pa_attend_chunk_workspace_size(g["q"].shape[0], g["tables"].shape[0],
+                                            g["q"].shape[1], g["max_chunk"], g["max_context"],
+                                            cache, window, partition_tokens)
+    ws = workspace
+    if ws == "own":
+        ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda") if need else None
+    out = g["out"].clone() if out is None else out
+    B.pa_attend_chunk(g["q"], g["k"], g["v"], g["cu"], g["tables"], g["lens"],
+                      g["scale"] if scale is None else scale, out, cache, g["max_chunk"],
+                      g["max_context"], window=window, partition_tokens=partition_tokens,
+                      workspace=ws, stream=stream)
+    return out
+
+
+def check(c, got, window=0, scale=None):
+    want, bound = attend_chunk(c["q"], c["k"], c["v"], c["cu"], c["tables"], c["lens"],
+                               c["scale"] if scale is None else scale, c["out"], window,
+                               c["k_scale"], c["v_scale"])
+    err = (got.cpu().double() - want).abs()
+    assert bool(torch.isfinite(got).all())
+    worst = float((err - bound).max())
+    assert worst <= 0, f"error {float(err.max())} passes the bound by {worst}"
+
+
+# (hq, hkv, d, bs, dtype, cache): head layouts, block sizes and types
+LAYOUTS = [
+    (8, 8, 64, 16, F16, "io"),
+    (4, 4, 128, 16, BF16, "io"),
+    (16, 2, 128, 16, BF16, "io"),
+    (6, 2, 64, 32, F16, "io"),      # 3 heads per KV head: 126 of a tile's 128 rows
+    (7, 1, 128, 8, BF16, "io"),
+    (4, 2, 128, 64, F16, "io"),
+    (4, 2, 64, 128, BF16, "io"),
+    (2, 1, 128, 256, F16, "io"),
+    (4, 2, 128, 4, F16, "io"),      # blocks too small for TMA boxes
+    (2, 1, 64, 1, BF16, "io"),
+    (8, 2, 128, 16, F16, "e4m3"),
+    (4, 1, 64, 32, BF16, "e4m3"),
+    (6, 2, 128, 2, F16, "e4m3"),
+    (130, 1, 64, 16, F16, "io"),    # more heads per KV head than a tile has rows
+]
+# (chunks, contexts)
+SHAPES = [
+    ([1], [1]),
+    ([3, 1, 5], [3, 70, 200]),
+    ([0, 4, 0, 1], [9, 130, 0, 1]),
+    ([40, 1, 0, 129], [300, 64, 5, 129]),
+]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=str)
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_matches_float64(layout, shape):
+    hq, hkv, d, bs, dtype, cache = layout
+    chunks, ctxs = SHAPES[shape]
+    c = chunk_case(len(chunks), hq, hkv, d, bs, dtype, chunks, ctxs, cache, pad=3, seed=shape)
+    g = on_gpu(c)
+    got = call(g)
+    assert B.pa_get_device_error() == 0
+    check(c, got)
+    assert torch.equal(got[int(c["cu"][-1]):].cpu(), c["out"][int(c["cu"][-1]):])
+
+
+@pytest.mark.parametrize("layout", [0, 2, 3, 8, 10, 11], ids=lambda i: str(LAYOUTS[i]))
+@pytest.mark.parametrize("window", [1, 7, 64, 100, 1000])
+@pytest.mark.parametrize("part", [0, 128])
+def test_window(layout, window, part):
+    hq, hkv, d, bs, dtype, cache = LAYOUTS[layout]
+    chunks, ctxs = [5, 1, 150], [400, 33, 310]
+    c = chunk_case(3, hq, hkv, d, bs, dtype, chunks, ctxs, cache, pad=1, seed=window)
+    # blocks the first row's window has left behind: freed, their entries anything
+    for b in range(3):
+        gone = max(0, ctxs[b] - chunks[b] - window + 1) // bs
+        for i in range(gone):
+            blk = int(c["tables"][b, i])
+            if cache == "e4m3":
+                c["k"][blk] = 0x7f
+                c["v"][blk] = 0x7f
+            else:
+                c["k"][blk] = float("nan")
+                c["v"][blk] = float("nan")
+    plain = dict(c)
+    plain["k"], plain["v"] = c["k"].clone(), c["v"].clone()
+    g = on_gpu(c)
+    for b in range(3):
+        gone = max(0, ctxs[b] - chunks[b] - window + 1) // bs
+        g["tables"][b, :gone] = -5
+    got = call(g, window=window, partition_tokens=part)
+    assert B.pa_get_device_error() == 0
+    check(plain, got, window)
+
+
+@pytest.mark.parametrize("layout", [1, 2, 5, 8, 10], ids=lambda i: str(LAYOUTS[i]))
+@pytest.mark.parametrize("part", [128, 256, 1024])
+def test_split_contexts(layout, part):
+    hq, hkv, d, bs, dtype, cache = LAYOUTS[layout]
+    c = chunk_case(3, hq, hkv, d, bs, dtype, [2, 70, 1], [700, 641, 1], cache, pad=2, seed=part)
+    got = call(on_gpu(c), partition_tokens=part)
+    assert B.pa_get_device_error() == 0
+    check(c, got)
+
+
+def test_many_sequences():
+    """More sequences than one probe of the tile search covers, with empty ones among them."""
+    n = 1100
+    chunks = [(i * 7) % 4 for i in range(n)]
+    ctxs = [c + (i % 40) for i, c in enumerate(chunks)]
+    c = chunk_case(n, 2, 1, 64, 16, F16, chunks, ctxs, pad=1)
+    got = call(on_gpu(c))
+    assert B.pa_get_device_error() == 0
+    check(c, got)
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0, 1e-6])
+def test_scales(scale):
+    c = chunk_case(2, 4, 2, 64, 16, F16, [9, 2], [50, 150])
+    got = call(on_gpu(c), scale=scale)
+    check(c, got, scale=scale)
+
+
+def test_infinite_keys_of_later_tokens():
+    """K of tokens a row does not see never reaches it, whatever its bits."""
+    c = chunk_case(1, 2, 1, 128, 16, BF16, [20], [90])
+    blk, row = int(c["tables"][0, 89 // 16]), 89 % 16
+    k = c["k"].clone()
+    k[blk, row] = float("inf")
+    g = on_gpu(dict(c, k=k))
+    got = call(g)
+    want, bound = attend_chunk(c["q"], c["k"], c["v"], c["cu"], c["tables"], c["lens"], c["scale"],
+                               c["out"])
+    err = (got.cpu().double() - want).abs()[:19]
+    assert bool((err <= bound[:19]).all())
+
+
+def test_one_token_chunks_agree_with_decode():
+    c = chunk_case(5, 8, 2, 128, 16, F16, [1] * 5, [1, 16, 17, 200, 333], junk=False)
+    g = on_gpu(c)
+    got = call(g)
+    out = torch.empty_like(got)
+    cache = cache_of(g)
+    need = B.pa_decode_workspace_size(5, 8, 333, cache)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    B.pa_decode(g["q"], g["k"], g["v"], g["tables"], g["lens"], c["scale"], out, cache, 333,
+                workspace=ws)
+    check(c, out)
+    check(c, got)
+
+
+def test_repeats_bit_for_bit_and_on_another_stream():
+    c = chunk_case(3, 8, 1, 128, 16, BF16, [33, 1, 6], [500, 64, 1000])
+    g = on_gpu(c)
+    a = call(g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b = g["out"].clone()
+    torch.cuda.synchronize()
+    call(g, stream=s, out=b)
+    s.synchronize()
+    assert torch.equal(a, b)
+    assert torch.equal(a, call(g))
+
+
+@pytest.mark.parametrize("cache", ["io", "e4m3"])
+def test_captured_and_replayed_with_new_inputs(cache):
+    c = chunk_case(2, 8, 2, 128, 16, F16, [4, 3], [900, 333], cache)
+    g = on_gpu(c)
+    cc = cache_of(g)
+    need = B.pa_attend_chunk_workspace_size(7, 2, 8, 4, 900, cc, 0, 128)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = g["out"].clone()
+    call(g, partition_tokens=128, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(g, partition_tokens=128, out=out, workspace=ws, stream=torch.cuda.current_stream())
+    # other queries, other lengths of the same launch
+    c2 = dict(c, q=torch.randn(c["q"].shape, generator=torch.Generator().manual_seed(5)).to(F16),
+              cu=torch.tensor([0, 1, 4], dtype=torch.int32),
+              lens=torch.tensor([700, 128], dtype=torch.int32))
+    g["q"].copy_(c2["q"])
+    g["cu"].copy_(c2["cu"])
+    g["lens"].copy_(c2["lens"])
+    out.copy_(c["out"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error() == 0
+    check(c2, out)
+
+
+def test_device_bounds_are_reported_not_faulted():
+    c = chunk_case(3, 4, 2, 64, 16, F16, [2, 3, 4], [40, 50, 60], pad=1)
+    def run(**change):
+        g = on_gpu(dict(c, **{k: v for k, v in change.items()}))
+        out = call(g)
+        return out.cpu(), B.pa_get_device_error()
+
+    ok, err = run()
+    assert err == 0
+    # a length shorter than its chunk, past max_context: zero rows, the others as before
+    for bad in (2, 61):
+        lens = torch.tensor([40, bad, 60], dtype=torch.int32)
+        g = on_gpu(dict(c, lens=lens))
+        out = call(g)
+        assert B.pa_get_device_error() == B.DEVERR_CONTEXT_LEN
+        assert bool((out[2:5] == 0).all())
+        assert torch.equal(out[:2].cpu(), ok[:2]) and torch.equal(out[5:].cpu(), ok[5:])
+    # a block id out of range
+    t = c["tables"].clone()
+    t[0, 1] = c["k"].shape[0]
+    out, err = run(tables=t)
+    assert err == B.DEVERR_BLOCK_ID and torch.equal(out[2:], ok[2:])
+    # row starts that run backwards, leave the rows, or a chunk past max_chunk
+    for cu in ([0, 2, 1, 9], [0, 2, 5, 12], [-1, 2, 5, 9], [0, 0, 5, 9]):
+        out, err = run(cu=torch.tensor(cu, dtype=torch.int32))
+        assert err & B.DEVERR_CHUNK, cu
+        assert torch.equal(out[9:], c["out"][9:]) or cu[-1] > 9
