@@ -74,7 +74,8 @@ typedef enum pa_status {
   PA_ERR_DEVICE_BOUNDS = 5  /* pa_get_device_error: a kernel saw an out-of-range value */
 } pa_status;
 
-typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2 } pa_dtype;
+/* (PA_F32: probabilities of pa_verify_draft only) */
+typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2, PA_F32 = 3 } pa_dtype;
 
 /* Bits of the device error word (pa_get_device_error). */
 #define PA_DEVERR_BLOCK_ID 0x1u    /* a block-table entry outside [0, num_blocks) */
@@ -86,6 +87,9 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2 } pa_dtype;
 #define PA_DEVERR_CHUNK 0x20u    /* pa_attend_chunk, pa_gather_kv, pa_verify_draft: row starts
                                       that run backwards, leave the rows given or exceed the
                                       stated maximum */
+#define PA_DEVERR_TOKEN 0x40u    /* pa_verify_draft: a drafted token outside the vocabulary */
+#define PA_DEVERR_PROBS 0x80u    /* pa_verify_draft: a row of probabilities without a positive,
+                                      finite value */
 #define PA_DEVERR_TIMEOUT 0x10u    /* a kernel's bounded wait for its own tensor-core
                                       work gave up (1 s); its results are not written */
 
@@ -397,6 +401,82 @@ pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, in
                           const int32_t* context_lens, int32_t max_context, int32_t window,
                           float scale, void* out, int32_t partition_tokens, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens (speculative decoding): which drafts the
+ * target keeps, and the token that follows them, from given random numbers.
+ * Sequence b has the drafts cu_drafts[b] .. cu_drafts[b + 1], in order. Draft
+ * t, token x, is accepted while every draft before it was and
+ *   accept_uniforms[t] * q_t(x) < p_t(x);
+ * the first refused draft is replaced by a draw from max(p - q, 0) of its
+ * position (from p where that is zero everywhere); if all are accepted, one
+ * more token is drawn from the row behind them. A draw takes the lowest
+ * token whose running sum of the weights exceeds sample_uniforms[b] times
+ * their total (sums in 64 bits). If the drafts were drawn from q, accepted
+ * drafts and the drawn token follow the target's distribution.
+ *   draft_tokens    [num_drafts] int32 in [0, vocab).
+ *   cu_drafts       [batch + 1] int32, not decreasing, within [0, num_drafts].
+ *   target_probs    [num_drafts + batch][vocab] in prob_dtype (PA_F32, PA_F16
+ *                   or PA_BF16): sequence b's rows start at cu_drafts[b] + b,
+ *                   one per draft and one behind the last. Rows need not be
+ *                   normalised; values that are not positive and finite count
+ *                   as zero.
+ *   draft_probs     [num_drafts][vocab] in prob_dtype, or NULL when drafts
+ *                   were chosen, not drawn (q is 1 at the draft).
+ *   accept_uniforms [num_drafts] fp32 in [0, 1).
+ *   sample_uniforms [batch] fp32 in [0, 1).
+ *   accepted        [batch] int32: accepted drafts a.
+ *   tokens          [batch][max_drafts + 1] int32: the a accepted drafts, the
+ *                   drawn token, then -1.
+ *   max_drafts      host-side upper bound of a sequence's drafts.
+ * A sequence outside its rows or with more than max_drafts drafts sets
+ * PA_DEVERR_CHUNK and is left as it was; a token outside the vocabulary sets
+ * PA_DEVERR_TOKEN and is refused; a row without weight sets PA_DEVERR_PROBS
+ * and gives token -1. Results are reproducible. */
+pa_status pa_verify_draft(const int32_t* draft_tokens, int64_t num_drafts, int32_t batch,
+                          const int32_t* cu_drafts, const void* target_probs,
+                          const void* draft_probs, int32_t prob_dtype, int32_t vocab,
+                          const float* accept_uniforms, const float* sample_uniforms,
+                          int32_t max_drafts, int32_t* accepted, int32_t* tokens, void* stream);
+
+/* Scales of an E4M3 cache from the K/V it is to hold (the KV cache article,
+ * section "再往后：压 KV 的三条路线": per-channel scaling factors from
+ * calibration). Per (head, channel), over the call's tokens and all earlier
+ * calls' on the same arrays:
+ *   amax = max(amax, max_t |x_t|),  scale = max(amax / 448, 2^-126),
+ *   inv_scale = 1 / scale;  scale = inv_scale = 1 while amax is 0.
+ *   k, v          [num_tokens][num_kv_heads][head_dim] in in_dtype.
+ *   slot_mapping  [num_tokens] int64 or NULL: tokens with slot < 0 (padding,
+ *                 as for pa_append_kv) do not count.
+ *   k_amax, v_amax  fp32 [num_kv_heads][head_dim], read and written; zeros
+ *                 before the first call.
+ *   k_scale, v_scale, k_inv_scale, v_inv_scale  fp32, written: the arrays of
+ *                 pa_cache_desc. Tokens appended under other scales keep their
+ *                 codes: calibrate before the cache is first written.
+ * Infinities and NaN do not count. num_tokens == 0 leaves amax and writes the
+ * scales. Every pointer is 16-byte aligned. */
+pa_status pa_calibrate_kv(const void* k, const void* v, int32_t in_dtype, int64_t num_tokens,
+                          int32_t num_kv_heads, int32_t head_dim, const int64_t* slot_mapping,
+                          float* k_amax, float* v_amax, float* k_scale, float* v_scale,
+                          float* k_inv_scale, float* v_inv_scale, void* stream);
+
+/* Read cached tokens back into contiguous rows: rows cu_tokens[b] ..
+ * cu_tokens[b + 1] of k_out / v_out receive sequence b's tokens from position
+ * first[b] on. A 16-bit cache's bits come back unchanged (out_dtype must be
+ * its dtype); an E4M3 cache's codes as e4m3(c) * scale in fp32, rounded to
+ * out_dtype (PA_F16 or PA_BF16). With pa_append_kv this moves sequences
+ * between caches (of other block sizes, dtypes or GPUs) or to host memory.
+ *   block_tables  [batch][max_blocks_per_seq] int32.
+ *   first         [batch] int32.
+ *   cu_tokens     [batch + 1] int32, not decreasing, within [0, num_tokens].
+ *   k_out, v_out  [num_tokens][num_kv_heads][head_dim]; rows outside
+ *                 cu_tokens[0] .. cu_tokens[batch] are left as they were.
+ * Row starts that run backwards or leave the rows set PA_DEVERR_CHUNK; a
+ * position below 0 or beyond the table sets PA_DEVERR_CONTEXT_LEN, a bad
+ * block id PA_DEVERR_BLOCK_ID, and such rows are zeros. */
+pa_status pa_gather_kv(const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                       const int32_t* first, const int32_t* cu_tokens, int64_t num_tokens,
+                       void* k_out, void* v_out, int32_t out_dtype, void* stream);
 
 /* Context parallelism, part 1: pa_decode over the tokens each sequence's
  * table lists, stopping short of the final normalisation across calls, so

@@ -18,12 +18,12 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpagedattn.so")
 
-PA_F16, PA_BF16, PA_E4M3 = 0, 1, 2
+PA_F16, PA_BF16, PA_E4M3, PA_F32 = 0, 1, 2, 3
 PA_OK = 0
 STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_CUDA",
           4: "PA_ERR_WORKSPACE", 5: "PA_ERR_DEVICE_BOUNDS"}
 DEVERR_BLOCK_ID, DEVERR_CONTEXT_LEN, DEVERR_SLOT, DEVERR_PREFIX = 0x1, 0x2, 0x4, 0x8
-DEVERR_TIMEOUT, DEVERR_CHUNK = 0x10, 0x20
+DEVERR_TIMEOUT, DEVERR_CHUNK, DEVERR_TOKEN, DEVERR_PROBS = 0x10, 0x20, 0x40, 0x80
 
 # names of every symbol include/pa_api.h declares
 EXPORTED = ["pa_append_kv", "pa_decode_workspace_size", "pa_decode_partition_tokens",
@@ -35,7 +35,7 @@ EXPORTED = ["pa_append_kv", "pa_decode_workspace_size", "pa_decode_partition_tok
             "pa_decode_shared_prefix_partition_tokens", "pa_testing_withhold_prefix_scores",
             "pa_set_deterministic", "pa_testing_withhold_steal_counts",
             "pa_decode_partial", "pa_merge_partials", "pa_attend_chunk_workspace_size",
-            "pa_attend_chunk"]
+            "pa_attend_chunk", "pa_verify_draft", "pa_calibrate_kv", "pa_gather_kv"]
 
 
 class PagedAttentionError(RuntimeError):
@@ -120,6 +120,12 @@ def load_library(path: str = LIB_PATH):
     lib.pa_attend_chunk.argtypes = [P, i32, i64, i32, i32, P, P, D, P, i32, P, i32, P, i32, i32,
                                     ctypes.c_float, P, i32, P, ctypes.c_size_t, P]
     lib.pa_attend_chunk.restype = ctypes.c_int
+    lib.pa_verify_draft.argtypes = [P, i64, i32, P, P, P, i32, i32, P, P, i32, P, P, P]
+    lib.pa_verify_draft.restype = ctypes.c_int
+    lib.pa_calibrate_kv.argtypes = [P, P, i32, i64, i32, i32, P, P, P, P, P, P, P, P]
+    lib.pa_calibrate_kv.restype = ctypes.c_int
+    lib.pa_gather_kv.argtypes = [P, P, D, P, i32, i32, P, P, i64, P, P, i32, P]
+    lib.pa_gather_kv.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -136,6 +142,7 @@ def _dtype_code(t: torch.dtype) -> int:
 
 _IO = (torch.float16, torch.bfloat16)
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_PROBS = (torch.float32, torch.float16, torch.bfloat16)
 
 
 def _on_device(t: torch.Tensor) -> bool:
@@ -449,6 +456,81 @@ def pa_attend_chunk(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, s
                              int(partition_tokens), _dev(workspace, "workspace"),
                              _nbytes(workspace), _stream(stream))
     _check(rc, "pa_attend_chunk")
+
+
+def pa_verify_draft(draft_tokens, cu_drafts, target_probs, draft_probs, accept_uniforms,
+                    sample_uniforms, accepted, tokens, stream=None):
+    """Which drafts the target keeps and the token behind them: draft_tokens
+    [N] int32, cu_drafts [batch + 1] int32, target_probs [N + batch, vocab]
+    and draft_probs [N, vocab] (or None: drafts chosen, not drawn) in one of
+    float32 / float16 / bfloat16, accept_uniforms [N] and sample_uniforms
+    [batch] float32. Writes accepted [batch] and tokens [batch, most + 1]
+    (accepted drafts, the drawn token, then -1), both int32."""
+    lib = load_library()
+    if target_probs.dim() != 2 or tokens.dim() != 2:
+        raise ValueError("target_probs: expected [num_drafts + batch, vocab]; tokens: expected "
+                         "[batch, max_drafts + 1]")
+    n, batch, vocab = draft_tokens.numel(), accepted.numel(), target_probs.shape[1]
+    if tokens.shape[1] < 1:
+        raise ValueError("tokens: expected [batch, max_drafts + 1]")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    pp = _dev(target_probs, "target_probs", _PROBS, (n + batch, vocab))
+    pq = _dev(draft_probs, "draft_probs", (target_probs.dtype,), (n, vocab))
+    rc = lib.pa_verify_draft(_dev(draft_tokens, "draft_tokens", i32, (n,)), n, batch,
+                             _dev(cu_drafts, "cu_drafts", i32, (batch + 1,)), pp, pq,
+                             PA_F32 if target_probs.dtype == torch.float32
+                             else _dtype_code(target_probs.dtype), vocab,
+                             _dev(accept_uniforms, "accept_uniforms", f32, (n,)),
+                             _dev(sample_uniforms, "sample_uniforms", f32, (batch,)),
+                             tokens.shape[1] - 1, _dev(accepted, "accepted", i32, (batch,)),
+                             _dev(tokens, "tokens", i32, (batch, tokens.shape[1])),
+                             _stream(stream))
+    _check(rc, "pa_verify_draft")
+
+
+def pa_calibrate_kv(k, v, slot_mapping, k_amax, v_amax, k_scale, v_scale, k_inv_scale,
+                    v_inv_scale, stream=None):
+    """E4M3 scales of the K/V a cache is to hold (k, v [T, Hkv, D], fp16 /
+    bf16): the running max-abs per (head, channel) in k_amax / v_amax, and
+    from it the scales and their inverses (all float32 [Hkv, D]). Tokens whose
+    slot_mapping ([T] int64, or None) is negative do not count."""
+    lib = load_library()
+    if k.dim() != 3:
+        raise ValueError("k: expected [num_tokens, num_kv_heads, head_dim]")
+    t, hkv, hd = k.shape
+    pk = _dev(k, "k", _IO, (t, hkv, hd))
+    pv = _dev(v, "v", (k.dtype,), (t, hkv, hd))
+    arrays = [_dev(a, name, (torch.float32,), (hkv, hd)) for a, name in
+              ((k_amax, "k_amax"), (v_amax, "v_amax"), (k_scale, "k_scale"),
+               (v_scale, "v_scale"), (k_inv_scale, "k_inv_scale"),
+               (v_inv_scale, "v_inv_scale"))]
+    rc = lib.pa_calibrate_kv(pk, pv, _dtype_code(k.dtype), t, hkv, hd,
+                             _dev(slot_mapping, "slot_mapping", (torch.int64,), (t,)), *arrays,
+                             _stream(stream))
+    _check(rc, "pa_calibrate_kv")
+
+
+def pa_gather_kv(k_cache, v_cache, block_tables, first, cu_tokens, k_out, v_out,
+                 cache: PagedCache, stream=None):
+    """Cached tokens back into contiguous rows: rows cu_tokens[b] ..
+    cu_tokens[b + 1] of k_out / v_out ([T, Hkv, D]) receive sequence b's
+    tokens from position first[b] on (an E4M3 cache's codes times their
+    scales). first: [batch] int32; cu_tokens: [batch + 1] int32."""
+    lib = load_library()
+    d = cache.desc()
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables: expected [batch, max_blocks_per_seq]")
+    batch, t = block_tables.shape[0], k_out.shape[0]
+    shape = (t, cache.num_kv_heads, cache.head_dim)
+    i32 = (torch.int32,)
+    kc, vc = cache.cache_ptrs(k_cache, v_cache)
+    rc = lib.pa_gather_kv(kc, vc, ctypes.byref(d), _dev(block_tables, "block_tables", i32),
+                          block_tables.shape[1], batch, _dev(first, "first", i32, (batch,)),
+                          _dev(cu_tokens, "cu_tokens", i32, (batch + 1,)), t,
+                          _dev(k_out, "k_out", _IO, shape),
+                          _dev(v_out, "v_out", (k_out.dtype,), shape), _dtype_code(k_out.dtype),
+                          _stream(stream))
+    _check(rc, "pa_gather_kv")
 
 
 def pa_copy_blocks(pairs, k_cache, v_cache, cache: PagedCache, stream=None):

@@ -20,11 +20,13 @@
 
 #include "pa_api.h"
 #include "pa_append_copy.cuh"
+#include "pa_calibrate_gather.cuh"
 #include "pa_chunk.cuh"
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
 #include "pa_prefix.cuh"
 #include "pa_prefix_umma.cuh"
+#include "pa_verify.cuh"
 
 namespace {
 
@@ -1032,6 +1034,147 @@ pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, in
   p.sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
   return q_dtype == PA_F16 ? launch_chunk<__half>(p, pl, cache, as_stream(stream))
                            : launch_chunk<__nv_bfloat16>(p, pl, cache, as_stream(stream));
+}
+
+pa_status pa_verify_draft(const int32_t* draft_tokens, int64_t num_drafts, int32_t batch,
+                          const int32_t* cu_drafts, const void* target_probs,
+                          const void* draft_probs, int32_t prob_dtype, int32_t vocab,
+                          const float* accept_uniforms, const float* sample_uniforms,
+                          int32_t max_drafts, int32_t* accepted, int32_t* tokens, void* stream) {
+  if (num_drafts < 0 || batch < 0 || vocab <= 0 || max_drafts < 0) return PA_ERR_INVALID_ARG;
+  if (prob_dtype != PA_F32 && prob_dtype != PA_F16 && prob_dtype != PA_BF16)
+    return PA_ERR_INVALID_ARG;
+  if (batch == 0) return PA_OK;
+  if (!cu_drafts || !target_probs || !sample_uniforms || !accepted || !tokens ||
+      (num_drafts > 0 && (!draft_tokens || !accept_uniforms)))
+    return PA_ERR_INVALID_ARG;
+  if (num_drafts > 0x7fffffffLL || batch > 0x7fffffff / pa::kVerifyCtas ||
+      max_drafts == 0x7fffffff)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t size = prob_dtype == PA_F32 ? 4 : 2;
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(target_probs) |
+                         reinterpret_cast<uintptr_t>(draft_probs);
+  if (addr % size != 0) return PA_ERR_INVALID_ARG;
+  pa::VerifyParams p{};
+  p.draft_tokens = draft_tokens;
+  p.cu_drafts = cu_drafts;
+  p.target_probs = target_probs;
+  p.draft_probs = draft_probs;
+  p.accept_uniforms = accept_uniforms;
+  p.sample_uniforms = sample_uniforms;
+  p.accepted = accepted;
+  p.tokens = tokens;
+  p.num_drafts = num_drafts;
+  p.vocab = vocab;
+  p.max_drafts = max_drafts;
+  const bool vec = addr % 16 == 0 && vocab * size % 16 == 0;
+  const cudaStream_t s = as_stream(stream);
+  const unsigned grid = static_cast<unsigned>(batch) * pa::kVerifyCtas;
+  auto go = [&](auto kern) {
+    kern<<<grid, pa::kVerifyThreads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  };
+  if (prob_dtype == PA_F32)
+    return vec ? go(pa::pa_verify_kernel<float, true>) : go(pa::pa_verify_kernel<float, false>);
+  if (prob_dtype == PA_F16)
+    return vec ? go(pa::pa_verify_kernel<__half, true>) : go(pa::pa_verify_kernel<__half, false>);
+  return vec ? go(pa::pa_verify_kernel<__nv_bfloat16, true>)
+             : go(pa::pa_verify_kernel<__nv_bfloat16, false>);
+}
+
+pa_status pa_calibrate_kv(const void* k, const void* v, int32_t in_dtype, int64_t num_tokens,
+                          int32_t num_kv_heads, int32_t head_dim, const int64_t* slot_mapping,
+                          float* k_amax, float* v_amax, float* k_scale, float* v_scale,
+                          float* k_inv_scale, float* v_inv_scale, void* stream) {
+  if (num_tokens < 0 || num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
+  if (in_dtype != PA_F16 && in_dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (num_tokens > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return PA_ERR_INVALID_ARG;
+  float* const arrays[6] = {k_amax, v_amax, k_scale, v_scale, k_inv_scale, v_inv_scale};
+  for (float* a : arrays)
+    if (!a || !aligned16(a)) return PA_ERR_INVALID_ARG;
+  pa::CalibrateParams p{};
+  p.x[0] = k, p.x[1] = v;
+  p.amax[0] = k_amax, p.amax[1] = v_amax;
+  p.scale[0] = k_scale, p.scale[1] = v_scale;
+  p.inv_scale[0] = k_inv_scale, p.inv_scale[1] = v_inv_scale;
+  p.slots = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.columns = num_kv_heads * head_dim;
+  const int groups = p.columns / 8;
+  const int width = std::min(groups, 256);
+  const int col_blocks = (groups + width - 1) / width;
+  const int rows = 256 / width;
+  // four CTAs per SM, at least 16 tokens for each of a CTA's threads
+  const int64_t want = std::max<int64_t>(1, 4 * kNumSMs / (2 * col_blocks));
+  const int64_t splits = std::max<int64_t>(
+      1, std::min<int64_t>(want, num_tokens / (16 * rows)));
+  p.tokens_per_split = std::max<int64_t>(1, (num_tokens + splits - 1) / splits);
+  const cudaStream_t s = as_stream(stream);
+  const dim3 grid(static_cast<unsigned>(splits), col_blocks, 2);
+  const bool bf16 = in_dtype == PA_BF16;
+  if (splits == 1) {
+    if (bf16)
+      pa::pa_calibrate_kernel<true, true><<<grid, 256, 0, s>>>(p);
+    else
+      pa::pa_calibrate_kernel<false, true><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  if (bf16)
+    pa::pa_calibrate_kernel<true, false><<<grid, 256, 0, s>>>(p);
+  else
+    pa::pa_calibrate_kernel<false, false><<<grid, 256, 0, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+  return launch_dependent(pa::pa_calibrate_scale_kernel, dim3((p.columns + 255) / 256, 2),
+                          dim3(256), 0, s, p) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_gather_kv(const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                       const int32_t* first, const int32_t* cu_tokens, int64_t num_tokens,
+                       void* k_out, void* v_out, int32_t out_dtype, void* stream) {
+  int bs_log2 = 0;
+  pa_status st = check_cache(cache, &bs_log2);
+  if (st != PA_OK) return st;
+  if (max_blocks_per_seq <= 0 || batch < 0 || num_tokens < 0) return PA_ERR_INVALID_ARG;
+  if (out_dtype != PA_F16 && out_dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+  if (cache->cache_dtype != PA_E4M3 && cache->cache_dtype != out_dtype) return PA_ERR_UNSUPPORTED;
+  if (batch == 0 || num_tokens == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !first || !cu_tokens || !k_out || !v_out)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+    return PA_ERR_INVALID_ARG;
+  if (cache->cache_dtype == PA_E4M3 && (!cache->k_scale || !cache->v_scale ||
+                                        !aligned16(cache->k_scale) || !aligned16(cache->v_scale)))
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0x7fffffffLL || cache->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  pa::GatherParams p{};
+  p.cache[0] = k_cache, p.cache[1] = v_cache;
+  p.out[0] = k_out, p.out[1] = v_out;
+  p.scale[0] = cache->k_scale, p.scale[1] = cache->v_scale;
+  p.block_tables = block_tables;
+  p.first = first;
+  p.cu = cu_tokens;
+  p.num_blocks = cache->num_blocks;
+  p.num_tokens = num_tokens;
+  p.batch = batch;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.bs_log2 = bs_log2;
+  p.columns = cache->num_kv_heads * cache->head_dim;
+  // 32 rows a CTA, 8 while that leaves fewer than two CTAs per SM
+  const int per = num_tokens >= 2 * kNumSMs * pa::kGatherTokens ? pa::kGatherTokens : 8;
+  const dim3 grid(static_cast<unsigned>((num_tokens + per - 1) / per));
+  const cudaStream_t s = as_stream(stream);
+  if (cache->cache_dtype != PA_E4M3)
+    pa::pa_gather_kernel<0><<<grid, 256, 0, s>>>(p, per);
+  else if (out_dtype == PA_F16)
+    pa::pa_gather_kernel<1><<<grid, 256, 0, s>>>(p, per);
+  else
+    pa::pa_gather_kernel<2><<<grid, 256, 0, s>>>(p, per);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_merge_partials(const float* part_o, const float* part_ml, int32_t num_parts,

@@ -110,3 +110,57 @@ def chunk_case(batch, hq, hkv, d, bs, dtype, chunks, ctxs, cache="io", pad=0, se
 
 def on_gpu(c, device="cuda"):
     return {k: v.to(device) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+
+
+def weight(x):
+    """A probability row in float64; what is not positive and finite counts as zero."""
+    x = x.double()
+    return torch.where((x > 0) & (x < math.inf), x, 0.0)
+
+
+def verify_draft(drafts, cu, target, draft, u_accept, u_sample, most):
+    """(accepted, tokens) by the definition, one sequence at a time."""
+    accepted, rows = [], []
+    for b in range(len(cu) - 1):
+        start, n = int(cu[b]), int(cu[b + 1]) - int(cu[b])
+        a = 0
+        while a < n:
+            x = int(drafts[start + a])
+            if not 0 <= x < target.shape[1]:
+                break
+            p = float(weight(target[start + b + a, x]))
+            q = 1.0 if draft is None else float(weight(draft[start + a, x]))
+            if not float(u_accept[start + a].double()) * q < p:
+                break
+            a += 1
+        p = weight(target[start + b + a])
+        w = p.clone()
+        if a < n:
+            if draft is None:
+                if 0 <= int(drafts[start + a]) < len(w):
+                    w[int(drafts[start + a])] = 0.0
+            else:
+                w = (p - weight(draft[start + a])).clamp(min=0.0)
+            if float(w.sum()) == 0.0:
+                w = p
+        token = -1
+        total = math.fsum(w.tolist())
+        if total > 0:
+            run = torch.cumsum(w, 0)
+            past = ((run > float(u_sample[b].double()) * total) & (w > 0)).nonzero()
+            token = int(past[0]) if len(past) else int((w > 0).nonzero()[-1])
+        accepted.append(a)
+        rows.append([int(drafts[start + i]) for i in range(a)] + [token] + [-1] * (most - a))
+    return accepted, rows
+
+
+def calibrate(x, slots, amax):
+    """(amax, scale, inv_scale) in float32, by the definition."""
+    x = x.double().abs()
+    x = torch.where(torch.isfinite(x), x, 0.0)
+    if slots is not None:
+        x = x[slots >= 0]
+    amax = torch.cat([amax.double()[None], x]).amax(0).float()
+    scale = (amax / 448.0).clamp(min=2.0 ** -126)
+    scale = torch.where(amax > 0, scale, 1.0)
+    return amax, scale, 1.0 / scale
