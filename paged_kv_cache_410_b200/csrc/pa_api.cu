@@ -839,6 +839,22 @@ ChunkPlan make_chunk_plan(int64_t num_tokens, int64_t batch, int64_t num_q_heads
   return pl;
 }
 
+// Whether `kern` was compiled for `regs` registers a thread: its warps move
+// registers between them, and an increase beyond what the launch holds would
+// wait for good.
+bool launches_with(const void* kern, int regs) {
+  static std::mutex mu;
+  static std::unordered_map<const void*, int> have;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = have.find(kern);
+  if (it == have.end()) {
+    cudaFuncAttributes a{};
+    if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) return false;
+    it = have.emplace(kern, a.numRegs).first;
+  }
+  return (it->second + 7) / 8 * 8 >= regs;
+}
+
 template <typename TQ, int D, int NT, int BN, int MODE>
 pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, cudaStream_t st) {
@@ -846,6 +862,7 @@ pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const 
   auto kern = pa::pa_chunk_kernel<TQ, D, NT, BN, MODE>;
   if (ensure_smem(reinterpret_cast<const void*>(kern), C::kRequest) != cudaSuccess)
     return PA_ERR_CUDA;
+  if (!launches_with(reinterpret_cast<const void*>(kern), C::kLaunchRegs)) return PA_ERR_CUDA;
   const int64_t ctas = static_cast<int64_t>(p.num_tiles) * p.num_kv_heads * p.head_blocks *
                        p.num_partitions;
   kern<<<static_cast<unsigned>(ctas), C::kThreads, C::kRequest, st>>>(p, tq, tk, tv);

@@ -129,11 +129,27 @@ constexpr int kChunkE4m3 = 2;    // cp.async of codes, widened to f16
 
 template <int D, int NT, int BN, int MODE>
 struct ChunkCfg {
+  // warps in groups of four (a register split is set per group): 4 NT softmax
+  // warps; with loader warps a group of them, then the MMA warp and three
+  // that idle; with TMA the producer, the MMA warp and two that idle
   static constexpr int kSoftmaxWarps = 4 * NT;
   static constexpr int kLoadWarps = MODE == kChunkTma ? 1 : 4;
   static constexpr int kLoadThreads = 32 * kLoadWarps;
   static constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kWarps = kSoftmaxWarps + (MODE == kChunkTma ? 4 : 8);
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM
+  // registers per thread: at launch (the register file over the CTAs' threads),
+  // then moved from the other groups to the softmax warps, which hold a row of
+  // BN scores each
+  static constexpr int kLaunchRegs = 65536 / (kCtas * kThreads) / 8 * 8;
+  static constexpr int kSoftmaxRegs =
+      MODE == kChunkTma ? (NT == 2 ? 208 : 152) : (NT == 2 ? 184 : 128);
+  static constexpr int kLoadRegs = MODE == kChunkTma ? (NT == 2 ? 80 : 104) : (NT == 2 ? 80 : 64);
+  static constexpr int kMmaRegs = MODE == kChunkTma ? kLoadRegs : (NT == 2 ? 64 : 48);
+  static_assert(kSoftmaxWarps * kSoftmaxRegs + 4 * kLoadRegs + (MODE == kChunkTma ? 0 : 4 * kMmaRegs) <=
+                    kWarps * kLaunchRegs,
+                "the split draws on the launch's registers");
   // TMEM columns: S (and P) of tile t at t * BN, O of tile t behind them
   static constexpr int kOCol = NT * BN;
   static constexpr int kColsUsed = kOCol + NT * D;
@@ -146,7 +162,6 @@ struct ChunkCfg {
   static constexpr int kRaw = MODE == kChunkE4m3 ? kBuf / 2 : 0;  // its E4M3 codes
   static constexpr int kRawStages = MODE == kChunkE4m3 ? (NT == 1 ? 3 : 4) : 0;
   // bytes for tiles: 224 KB for one CTA per SM, 111 KB for two
-  static constexpr int kCtas = NT == 1 ? 2 : 1;
   static constexpr int kBudget = kCtas == 2 ? 111 * 1024 : 224 * 1024;
   static constexpr int kFit = (kBudget - NT * kQTile - kRawStages * kRaw) / kBuf;
   static constexpr int kBufs = kFit < 8 ? kFit : 8;
@@ -178,6 +193,21 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// The larger of three; NaN if any is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void set_more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
 // Grid: tiles x KV heads x head blocks x partitions, partition fastest, the
@@ -308,220 +338,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
     if (nsteps > 0 && lane == 0) mbar_wait(bar_q, 0);
   };
 
-  if (warp >= C::kSoftmaxWarps && warp < C::kMmaWarp) {
-    if constexpr (MODE == kChunkTma) {
-      // ---- TMA producer: lane i issues box (unit i / SLABS, slab i % SLABS) ----
-      if (lane == 0) {
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
-      }
-      const int bs_mask = (1 << p.bs_log2) - 1;
-      const int unit = min(1 << p.bs_log2, BN);
-      const int nbox = BN / unit * SLABS;  // <= 32
-      const int u0 = lane / SLABS * unit;
-      const int sl = lane % SLABS;
-      // slot of this lane's unit in step `it`; units without a token of
-      // [lo, hi), and bad blocks, read past the map: zeros. Their table
-      // entries are not looked up.
-      auto slot_of = [&](int it) -> int {
-        const int j = c0 + it * BN + u0;
-        if (lane >= nbox || j >= c1 || j + unit <= ct.lo) return p.num_slots;
-        const int blk = block_of(j);
-        return blk < 0 ? p.num_slots : (blk << p.bs_log2) + (j & bs_mask);
-      };
-      auto load = [&](const CUtensorMap* map, int n, int slot) {
-        const uint32_t bar = bar_full + 8 * (n % NBUF);
-        if (lane == 0) mbar_arrive_expect_tx(bar, C::kBuf);
-        __syncwarp();
-        if (lane < nbox) tma_load_3d(buf(n) + sl * C::kBufSlab + u0 * 128, map, bar, sl * 64, hk, slot);
-      };
-      load_q();
-      int issued = 0;
-      int slot = nsteps > 0 ? slot_of(0) : 0;
-      for (int it = 0; it < nsteps && ok; ++it) {
-        const int next = it + 1 < nsteps ? slot_of(it + 1) : 0;
-        for (int n = 2 * it; n < 2 * it + 2; ++n) {
-          if (n >= NBUF &&
-              !__all_sync(0xffffffffu, mbar_wait_or_abort(bar_free + 8 * (n % NBUF),
-                                                          parity(n - NBUF), abort))) {
-            ok = false;
-            break;
-          }
-          load((n & 1) ? &tm_v : &tm_k, n, slot);
-          issued = n + 1;
-        }
-        slot = next;
-      }
-      // every issued copy has landed before the CTA can exit
-      if (lane == 0) {
-        for (int n = max(issued - NBUF, 0); n < issued; ++n)
-          mbar_wait(bar_full + 8 * (n % NBUF), parity(n));
-      }
-      drain_q();
-    } else {
-      // ---- loader warps: 16-byte pieces with cp.async -------------------------
-      const int lt = tid - C::kSoftmaxWarps * 32;
-      constexpr int kElem = MODE == kChunkE4m3 ? 1 : 2;
-      constexpr int kPieces = D * kElem / 16;            // per token row
-      constexpr int kPer = BN * kPieces / C::kLoadThreads;  // per thread and step
-      static_assert(kPer * C::kLoadThreads == BN * kPieces, "whole rounds");
-      const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D * kElem;
-      const uint32_t sRaw = base + C::kRawOff;
-      // start the copies of ring buffer n (into the raw stage, or the buffer
-      // itself); tokens outside [lo, c1) and bad blocks become zeros
-      auto start = [&](int n) {
-        const char* cache = reinterpret_cast<const char*>((n & 1) ? p.v_cache : p.k_cache);
-        int64_t slot[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int j = c0 + (n >> 1) * BN + (lt + k * C::kLoadThreads) / kPieces;
-          slot[k] = -1;
-          if (j >= ct.lo && j < c1) {
-            const int blk = block_of(j);
-            if (blk >= 0)
-              slot[k] = (static_cast<int64_t>(blk) << p.bs_log2) + (j & ((1 << p.bs_log2) - 1));
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int piece = lt + k * C::kLoadThreads;
-          const int r = piece / kPieces, c = piece % kPieces;
-          const char* src = slot[k] < 0 ? cache : cache + slot[k] * row_bytes + hk * (D * kElem) + c * 16;
-          uint32_t dst;
-          if constexpr (MODE == kChunkE4m3)
-            dst = sRaw + (n % C::kRawStages) * C::kRaw + piece * 16;
-          else
-            dst = buf(n) + (c >> 3) * C::kBufSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          cp_async_16(dst, src, slot[k] < 0 ? 0u : 16u);
-        }
-      };
-      // finish buffer n: its copies (this thread's own) have landed
-      auto finish = [&](int n) {
-        if constexpr (MODE == kChunkE4m3) {
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int piece = lt + k * C::kLoadThreads;
-            const int r = piece / kPieces, c = piece % kPieces;
-            const uint4 w = lds128(sRaw + (n % C::kRawStages) * C::kRaw + piece * 16);
-            uint4 h[2];
-            e4m3x4_to_f16x2x2(w.x, h[0].x, h[0].y);
-            e4m3x4_to_f16x2x2(w.y, h[0].z, h[0].w);
-            e4m3x4_to_f16x2x2(w.z, h[1].x, h[1].y);
-            e4m3x4_to_f16x2x2(w.w, h[1].z, h[1].w);
-            // the row's two slabs would meet in the same banks: the upper
-            // slab's threads store their odd half first
-            const bool odd = c >= 4;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int half = e ^ (odd ? 1 : 0);
-              const int cc = 2 * c + half;
-              const uint4 v = half ? h[1] : h[0];
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(
-                               buf(n) + (cc >> 3) * C::kBufSlab + r * 128 +
-                               (((cc & 7) ^ (r & 7)) << 4)),
-                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                           : "memory");
-            }
-          }
-        }
-        fence_async_smem();
-        mbar_arrive(bar_full + 8 * (n % NBUF));
-      };
-      // copies run kAhead buffers ahead of their use
-      constexpr int kAhead = MODE == kChunkE4m3 ? C::kRawStages - 1 : NBUF - 2;
-      const int total = 2 * nsteps;
-      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) load_q();
-      auto wait_free = [&](int n) {
-        return n < NBUF || mbar_wait_or_abort(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
-      };
-      for (int n = 0; n < total + kAhead; ++n) {
-        if (n < total) {
-          if (MODE == kChunkCopy && !wait_free(n)) break;
-          start(n);
-        }
-        cp_async_commit();
-        const int m = n - kAhead;
-        if (m >= 0) {
-          cp_async_wait<kAhead>();
-          if (MODE == kChunkE4m3 && !wait_free(m)) break;
-          finish(m);
-        }
-      }
-      cp_async_wait<0>();
-      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) drain_q();
-    }
-  } else if (warp == C::kMmaWarp) {
-    // ---- MMA issue --------------------------------------------------------------
-    // MMAs of one thread run in issue order, so S(it + 1) may follow the P.V(it)
-    // that reads P from the same columns, and a full S also says that the
-    // tile's earlier P.V are done.
-    if (lane == 0 && nsteps > 0) {
-      int a[NT], b[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        a[t] = t < ntiles ? tile_a(t) : 0;
-        b[t] = t < ntiles ? tile_b(t) : 0;
-      }
-      auto full = [&](int n) {
-        return mbar_wait_or_abort(bar_full + 8 * (n % NBUF), parity(n), abort);
-      };
-      auto issue_s = [&](int t, int it) {
-        const uint32_t k = buf(2 * it);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t ad = sw128_desc(
-              sQ + t * C::kQTile + (kk >> 2) * (kUmmaRows * 128) + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd = sw128_desc(k + (kk >> 2) * C::kBufSlab + (kk & 3) * 32, 16, 1024);
-          umma_f16(tmem + t * BN, ad, bd, kIdescS, kk > 0);
-        }
-        umma_commit(bar_s + 8 * t);
-      };
-      ok = mbar_wait_or_abort(bar_q, 0, abort) && full(0);
-      tc_fence_after();
-      if (ok) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (a[t] == 0 && b[t] > 0) issue_s(t, 0);
-        umma_commit(bar_free);
-      }
-      for (int it = 0; ok && it < nsteps; ++it) {
-        const uint32_t v = buf(2 * it + 1);
-        const bool more = it + 1 < nsteps;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (ok && it >= a[t] && it < b[t]) {
-            ok = mbar_wait_or_abort(bar_p + 8 * t, static_cast<uint32_t>((it - a[t]) & 1), abort) &&
-                 full(2 * it + 1);
-            if (ok) {
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                umma_f16_tmem_a(tmem + C::kOCol + t * D, tmem + t * BN + kk * 8,
-                                sw128_desc(v + kk * 16 * 128, C::kBufSlab, 1024), kIdescPV,
-                                (it > a[t] || kk > 0) ? 1u : 0u);
-              if (it == b[t] - 1) umma_commit(bar_o + 8 * t);
-            }
-          }
-          if (ok && more && it + 1 >= a[t] && it + 1 < b[t]) {
-            ok = full(2 * it + 2);
-            if (ok) {
-              tc_fence_after();
-              issue_s(t, it + 1);
-            }
-          }
-        }
-        if (!ok || !full(2 * it + 1)) break;
-        umma_commit(bar_free + 8 * ((2 * it + 1) % NBUF));
-        if (more) {
-          if (!full(2 * it + 2)) break;
-          umma_commit(bar_free + 8 * ((2 * it + 2) % NBUF));
-        }
-      }
-      // every issued MMA has completed before TMEM is released
-      umma_commit(bar_done);
-      mbar_wait(bar_done, 0);
-    }
-  } else {
+  // (one register change per group of four warps, at one place)
+  if (warp < C::kSoftmaxWarps) {
+    set_more_regs<C::kSoftmaxRegs>();
     // ---- softmax: thread = row ----------------------------------------------------
     const int tile = warp >> 2;
     const int my_row = tid & (kUmmaRows - 1);
@@ -619,19 +438,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
           for (int j = 0; j < BN; ++j)
             if (j > up || j < dn) s[j] = -INFINITY;
         }
-        float m8[8];
+        // the row's maximum in four chains of three-input maxima; NaN if a score is
+        float m4[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = s[i];
+        for (int i = 0; i < 4; ++i) m4[i] = max3_nan(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
 #pragma unroll
-        for (int j = 8; j < BN; ++j) m8[j & 7] = fmaxf(m8[j & 7], s[j]);
-        float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                         fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        for (int j = 12; j + 1 < BN; j += 2) m4[(j >> 1) & 3] = max3_nan(m4[(j >> 1) & 3], s[j], s[j + 1]);
+        float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
         mx *= scale_log2;
         const bool up = mx > m_run + kRescaleLog2;  // (the first finite maximum always moves it)
         const float m_ref = up ? mx : m_run;
         const float alpha = up ? ex2(m_run - m_ref) : 1.f;
         // a row that has seen no token yet keeps p = 2^(-inf) = 0
-        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float neg_m = mx != mx ? mx : m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t sc2 = pack_f32x2(scale_log2, scale_log2);
         const uint64_t nm2 = pack_f32x2(neg_m, neg_m);
         uint64_t sum2[2] = {0ull, 0ull};
@@ -734,6 +553,223 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
       }
       if (live && p.num_partitions > 1)
         p.ws_ml[row * p.num_partitions + part] = make_float2(m_run, l_run);
+    }
+  } else if (MODE != kChunkTma && warp < C::kMmaWarp) {
+    set_fewer_regs<C::kLoadRegs>();
+    if constexpr (MODE != kChunkTma) {
+      // ---- loader warps: 16-byte pieces with cp.async -------------------------
+      const int lt = tid - C::kSoftmaxWarps * 32;
+      constexpr int kElem = MODE == kChunkE4m3 ? 1 : 2;
+      constexpr int kPieces = D * kElem / 16;            // per token row
+      constexpr int kPer = BN * kPieces / C::kLoadThreads;  // per thread and step
+      static_assert(kPer * C::kLoadThreads == BN * kPieces, "whole rounds");
+      const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D * kElem;
+      const uint32_t sRaw = base + C::kRawOff;
+      // start the copies of ring buffer n (into the raw stage, or the buffer
+      // itself); tokens outside [lo, c1) and bad blocks become zeros
+      auto start = [&](int n) {
+        const char* cache = reinterpret_cast<const char*>((n & 1) ? p.v_cache : p.k_cache);
+        int64_t slot[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int j = c0 + (n >> 1) * BN + (lt + k * C::kLoadThreads) / kPieces;
+          slot[k] = -1;
+          if (j >= ct.lo && j < c1) {
+            const int blk = block_of(j);
+            if (blk >= 0)
+              slot[k] = (static_cast<int64_t>(blk) << p.bs_log2) + (j & ((1 << p.bs_log2) - 1));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int piece = lt + k * C::kLoadThreads;
+          const int r = piece / kPieces, c = piece % kPieces;
+          const char* src = slot[k] < 0 ? cache : cache + slot[k] * row_bytes + hk * (D * kElem) + c * 16;
+          uint32_t dst;
+          if constexpr (MODE == kChunkE4m3)
+            dst = sRaw + (n % C::kRawStages) * C::kRaw + piece * 16;
+          else
+            dst = buf(n) + (c >> 3) * C::kBufSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          cp_async_16(dst, src, slot[k] < 0 ? 0u : 16u);
+        }
+      };
+      // finish buffer n: its copies (this thread's own) have landed
+      auto finish = [&](int n) {
+        if constexpr (MODE == kChunkE4m3) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int piece = lt + k * C::kLoadThreads;
+            const int r = piece / kPieces, c = piece % kPieces;
+            const uint4 w = lds128(sRaw + (n % C::kRawStages) * C::kRaw + piece * 16);
+            uint4 h[2];
+            e4m3x4_to_f16x2x2(w.x, h[0].x, h[0].y);
+            e4m3x4_to_f16x2x2(w.y, h[0].z, h[0].w);
+            e4m3x4_to_f16x2x2(w.z, h[1].x, h[1].y);
+            e4m3x4_to_f16x2x2(w.w, h[1].z, h[1].w);
+            // the row's two slabs would meet in the same banks: the upper
+            // slab's threads store their odd half first
+            const bool odd = c >= 4;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int half = e ^ (odd ? 1 : 0);
+              const int cc = 2 * c + half;
+              const uint4 v = half ? h[1] : h[0];
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                               buf(n) + (cc >> 3) * C::kBufSlab + r * 128 +
+                               (((cc & 7) ^ (r & 7)) << 4)),
+                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
+            }
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(bar_full + 8 * (n % NBUF));
+      };
+      // copies run kAhead buffers ahead of their use
+      constexpr int kAhead = MODE == kChunkE4m3 ? C::kRawStages - 1 : NBUF - 2;
+      const int total = 2 * nsteps;
+      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) load_q();
+      auto wait_free = [&](int n) {
+        return n < NBUF || mbar_wait_or_abort(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
+      };
+      for (int n = 0; n < total + kAhead; ++n) {
+        if (n < total) {
+          if (MODE == kChunkCopy && !wait_free(n)) break;
+          start(n);
+        }
+        cp_async_commit();
+        const int m = n - kAhead;
+        if (m >= 0) {
+          cp_async_wait<kAhead>();
+          if (MODE == kChunkE4m3 && !wait_free(m)) break;
+          finish(m);
+        }
+      }
+      cp_async_wait<0>();
+      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) drain_q();
+    }
+  } else {
+    set_fewer_regs<C::kMmaRegs>();
+    if (warp == C::kMmaWarp) {
+      // ---- MMA issue --------------------------------------------------------------
+      // MMAs of one thread run in issue order, so S(it + 1) may follow the P.V(it)
+      // that reads P from the same columns, and a full S also says that the
+      // tile's earlier P.V are done.
+      if (lane == 0 && nsteps > 0) {
+        int a[NT], b[NT];
+  #pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          a[t] = t < ntiles ? tile_a(t) : 0;
+          b[t] = t < ntiles ? tile_b(t) : 0;
+        }
+        auto full = [&](int n) {
+          return mbar_wait_or_abort(bar_full + 8 * (n % NBUF), parity(n), abort);
+        };
+        auto issue_s = [&](int t, int it) {
+          const uint32_t k = buf(2 * it);
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t ad = sw128_desc(
+                sQ + t * C::kQTile + (kk >> 2) * (kUmmaRows * 128) + (kk & 3) * 32, 16, 1024);
+            const uint64_t bd = sw128_desc(k + (kk >> 2) * C::kBufSlab + (kk & 3) * 32, 16, 1024);
+            umma_f16(tmem + t * BN, ad, bd, kIdescS, kk > 0);
+          }
+          umma_commit(bar_s + 8 * t);
+        };
+        ok = mbar_wait_or_abort(bar_q, 0, abort) && full(0);
+        tc_fence_after();
+        if (ok) {
+  #pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (a[t] == 0 && b[t] > 0) issue_s(t, 0);
+          umma_commit(bar_free);
+        }
+        for (int it = 0; ok && it < nsteps; ++it) {
+          const uint32_t v = buf(2 * it + 1);
+          const bool more = it + 1 < nsteps;
+  #pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (ok && it >= a[t] && it < b[t]) {
+              ok = mbar_wait_or_abort(bar_p + 8 * t, static_cast<uint32_t>((it - a[t]) & 1), abort) &&
+                   full(2 * it + 1);
+              if (ok) {
+                tc_fence_after();
+  #pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                  umma_f16_tmem_a(tmem + C::kOCol + t * D, tmem + t * BN + kk * 8,
+                                  sw128_desc(v + kk * 16 * 128, C::kBufSlab, 1024), kIdescPV,
+                                  (it > a[t] || kk > 0) ? 1u : 0u);
+                if (it == b[t] - 1) umma_commit(bar_o + 8 * t);
+              }
+            }
+            if (ok && more && it + 1 >= a[t] && it + 1 < b[t]) {
+              ok = full(2 * it + 2);
+              if (ok) {
+                tc_fence_after();
+                issue_s(t, it + 1);
+              }
+            }
+          }
+          if (!ok || !full(2 * it + 1)) break;
+          umma_commit(bar_free + 8 * ((2 * it + 1) % NBUF));
+          if (more) {
+            if (!full(2 * it + 2)) break;
+            umma_commit(bar_free + 8 * ((2 * it + 2) % NBUF));
+          }
+        }
+        // every issued MMA has completed before TMEM is released
+        umma_commit(bar_done);
+        mbar_wait(bar_done, 0);
+      }
+    } else if (MODE == kChunkTma && warp == C::kSoftmaxWarps) {
+      // ---- TMA producer: lane i issues box (unit i / SLABS, slab i % SLABS) ----
+      if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+      }
+      const int bs_mask = (1 << p.bs_log2) - 1;
+      const int unit = min(1 << p.bs_log2, BN);
+      const int nbox = BN / unit * SLABS;  // <= 32
+      const int u0 = lane / SLABS * unit;
+      const int sl = lane % SLABS;
+      // slot of this lane's unit in step `it`; units without a token of
+      // [lo, hi), and bad blocks, read past the map: zeros. Their table
+      // entries are not looked up.
+      auto slot_of = [&](int it) -> int {
+        const int j = c0 + it * BN + u0;
+        if (lane >= nbox || j >= c1 || j + unit <= ct.lo) return p.num_slots;
+        const int blk = block_of(j);
+        return blk < 0 ? p.num_slots : (blk << p.bs_log2) + (j & bs_mask);
+      };
+      auto load = [&](const CUtensorMap* map, int n, int slot) {
+        const uint32_t bar = bar_full + 8 * (n % NBUF);
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kBuf);
+        __syncwarp();
+        if (lane < nbox) tma_load_3d(buf(n) + sl * C::kBufSlab + u0 * 128, map, bar, sl * 64, hk, slot);
+      };
+      load_q();
+      int issued = 0;
+      int slot = nsteps > 0 ? slot_of(0) : 0;
+      for (int it = 0; it < nsteps && ok; ++it) {
+        const int next = it + 1 < nsteps ? slot_of(it + 1) : 0;
+        for (int n = 2 * it; n < 2 * it + 2; ++n) {
+          if (n >= NBUF &&
+              !__all_sync(0xffffffffu, mbar_wait_or_abort(bar_free + 8 * (n % NBUF),
+                                                          parity(n - NBUF), abort))) {
+            ok = false;
+            break;
+          }
+          load((n & 1) ? &tm_v : &tm_k, n, slot);
+          issued = n + 1;
+        }
+        slot = next;
+      }
+      // every issued copy has landed before the CTA can exit
+      if (lane == 0) {
+        for (int n = max(issued - NBUF, 0); n < issued; ++n)
+          mbar_wait(bar_full + 8 * (n % NBUF), parity(n));
+      }
+      drain_q();
     }
   }
 
