@@ -785,13 +785,13 @@ pa_status launch_cascade_d(const pa::DecodeParams& p, const CascadePlan& pl,
 
 // ---- chunk attention ----------------------------------------------------------
 // Rows (token, query head) of one KV head go into row tiles of 128. Chunks
-// that fit one tile per KV head (drafts) take one-tile CTAs, two per SM, and
-// steps of 64 tokens: each reads its tokens once and is bound by HBM. Longer
-// chunks take two tiles per CTA and steps of 128 tokens, so that every K/V
-// step serves 256 rows and one tile's softmax runs beside the other's MMAs.
+// that fit one tile per KV head (drafts) take one-tile CTAs, two per SM: each
+// reads its tokens once and is bound by HBM. Longer chunks take two tiles per
+// CTA, so that every K/V step serves 256 rows and one tile's softmax runs
+// beside the other's MMAs.
 struct ChunkPlan {
   int head_rows, head_blocks, tile_tokens;
-  int tiles_per_cta, step;
+  int tiles_per_cta;
   int num_tiles;
   int partition_tokens, num_partitions;
   size_t ws_o_bytes, ws_bytes;
@@ -807,13 +807,12 @@ ChunkPlan make_chunk_plan(int64_t num_tokens, int64_t batch, int64_t num_q_heads
   pl.head_blocks = static_cast<int>((group + pl.head_rows - 1) / pl.head_rows);
   pl.tile_tokens = pa::kUmmaRows / pl.head_rows;
   pl.tiles_per_cta = max_chunk > pl.tile_tokens ? 2 : 1;
-  pl.step = pl.tiles_per_cta == 2 ? 128 : 64;
   const int64_t t = static_cast<int64_t>(pl.tiles_per_cta) * pl.tile_tokens;
   const int64_t tiles = num_tokens / t + batch;  // chunk_tile's bound
   pl.num_tiles = static_cast<int>(tiles);
   // tokens a CTA tile can attend, from its first (rounded) token
   int64_t span = std::max<int64_t>(max_context, 1);
-  if (window > 0) span = std::min<int64_t>(span, window + t + pl.step);
+  if (window > 0) span = std::min<int64_t>(span, window + t + pa::kChunkStep);
   const int64_t heads = static_cast<int64_t>(cd->num_kv_heads) * pl.head_blocks;
   // CTAs with rows, when every chunk is as long as it can be
   const int64_t units =
@@ -855,11 +854,11 @@ bool launches_with(const void* kern, int regs) {
   return (it->second + 7) / 8 * 8 >= regs;
 }
 
-template <typename TQ, int D, int NT, int BN, int MODE>
+template <typename TQ, int D, int NT, int MODE>
 pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, cudaStream_t st) {
-  using C = pa::ChunkCfg<D, NT, BN, MODE>;
-  auto kern = pa::pa_chunk_kernel<TQ, D, NT, BN, MODE>;
+  using C = pa::ChunkCfg<D, NT, MODE>;
+  auto kern = pa::pa_chunk_kernel<TQ, D, NT, MODE>;
   if (ensure_smem(reinterpret_cast<const void*>(kern), C::kRequest) != cudaSuccess)
     return PA_ERR_CUDA;
   if (!launches_with(reinterpret_cast<const void*>(kern), C::kLaunchRegs)) return PA_ERR_CUDA;
@@ -872,7 +871,7 @@ pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const 
   if ((rows + 7) / 8 > 65535) return PA_ERR_UNSUPPORTED;
   return launch_dependent(pa::pa_chunk_merge_kernel<TQ, D>,
                           dim3(p.num_tiles, static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,
-                          st, p, NT * p.tile_tokens, BN) == cudaSuccess
+                          st, p, NT * p.tile_tokens) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }
@@ -892,7 +891,7 @@ pa_status launch_chunk_m(const pa::ChunkParams& p, const ChunkPlan& pl, cudaStre
     return PA_ERR_CUDA;
   if (MODE == pa::kChunkTma) {
     // caches [slot][Hkv][D]: 64 channels x 1 head x the tokens of a block (or step)
-    const uint32_t unit = static_cast<uint32_t>(std::min(1 << p.bs_log2, pl.step));
+    const uint32_t unit = static_cast<uint32_t>(std::min(1 << p.bs_log2, pa::kChunkStep));
     const uint64_t heads = static_cast<uint64_t>(p.num_kv_heads);
     const uint64_t slots = static_cast<uint64_t>(p.num_slots);
     if (!make_map_3d(&tk, kBF16, p.k_cache, {static_cast<uint64_t>(D), heads, slots},
@@ -901,8 +900,8 @@ pa_status launch_chunk_m(const pa::ChunkParams& p, const ChunkPlan& pl, cudaStre
                      {row, row * heads}, {64u, 1u, unit}))
       return PA_ERR_CUDA;
   }
-  return pl.tiles_per_cta == 2 ? launch_chunk_t<TQ, D, 2, 128, MODE>(p, tq, tk, tv, st)
-                               : launch_chunk_t<TQ, D, 1, 64, MODE>(p, tq, tk, tv, st);
+  return pl.tiles_per_cta == 2 ? launch_chunk_t<TQ, D, 2, MODE>(p, tq, tk, tv, st)
+                               : launch_chunk_t<TQ, D, 1, MODE>(p, tq, tk, tv, st);
 }
 
 template <typename TQ>

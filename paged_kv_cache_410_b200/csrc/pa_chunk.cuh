@@ -29,6 +29,8 @@
 
 namespace pa {
 
+constexpr int kChunkStep = 64;  // cached tokens per step
+
 struct ChunkParams {
   const void* q;              // [num_tokens][Hq][D]
   void* out;                  // [num_tokens][Hq][D]
@@ -78,7 +80,7 @@ struct ChunkTile {
 // b owns tile indices from f(b) = cu[b] / t + b (t tokens per tile), which
 // leaves it at least ceil(n_b / t) of them; surplus tiles have no rows. One
 // warp finds b, the last sequence with f(b) <= x, 32 probes at a time.
-__device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int t, int step) {
+__device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = p.batch;
   while (hi - lo > 1) {
@@ -118,7 +120,7 @@ __device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int
   c.pos0 = L - n + c.i0;
   c.hi = c.pos0 + c.tokens;
   c.lo = p.window > 0 ? max(0, c.pos0 - p.window + 1) : 0;
-  c.base = c.lo / step * step;
+  c.base = c.lo / kChunkStep * kChunkStep;
   return c;
 }
 
@@ -127,16 +129,22 @@ constexpr int kChunkTma = 0;     // TMA boxes (16-bit, blocks >= 8)
 constexpr int kChunkCopy = 1;    // cp.async (16-bit, smaller blocks)
 constexpr int kChunkE4m3 = 2;    // cp.async of codes, widened to f16
 
-template <int D, int NT, int BN, int MODE>
+#ifndef PA_CHUNK_FMA_EXP
+#define PA_CHUNK_FMA_EXP 4
+#endif
+
+template <int D, int NT, int MODE>
 struct ChunkCfg {
+  static constexpr int BN = kChunkStep;
   // warps in groups of four (a register split is set per group): 4 NT softmax
-  // warps; with loader warps a group of them, then the MMA warp and three
-  // that idle; with TMA the producer, the MMA warp and two that idle
+  // warps; two TMA producers (K, V) or four loader warps; a warp per tile that
+  // issues its S, and one per tile that issues its P.V; idle ones
   static constexpr int kSoftmaxWarps = 4 * NT;
-  static constexpr int kLoadWarps = MODE == kChunkTma ? 1 : 4;
+  static constexpr int kLoadWarps = MODE == kChunkTma ? 2 : 4;
   static constexpr int kLoadThreads = 32 * kLoadWarps;
-  static constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-  static constexpr int kWarps = kSoftmaxWarps + (MODE == kChunkTma ? 4 : 8);
+  static constexpr int kSWarp = kSoftmaxWarps + kLoadWarps;
+  static constexpr int kPvWarp = kSWarp + NT;
+  static constexpr int kWarps = (kPvWarp + NT + 3) / 4 * 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM
   // registers per thread: at launch (the register file over the CTAs' threads),
@@ -144,14 +152,13 @@ struct ChunkCfg {
   // BN scores each
   static constexpr int kLaunchRegs = 65536 / (kCtas * kThreads) / 8 * 8;
   static constexpr int kSoftmaxRegs =
-      MODE == kChunkTma ? (NT == 2 ? 208 : 152) : (NT == 2 ? 184 : 128);
-  static constexpr int kLoadRegs = MODE == kChunkTma ? (NT == 2 ? 80 : 104) : (NT == 2 ? 80 : 64);
-  static constexpr int kMmaRegs = MODE == kChunkTma ? kLoadRegs : (NT == 2 ? 64 : 48);
-  static_assert(kSoftmaxWarps * kSoftmaxRegs + 4 * kLoadRegs + (MODE == kChunkTma ? 0 : 4 * kMmaRegs) <=
-                    kWarps * kLaunchRegs,
-                "the split draws on the launch's registers");
-  // TMEM columns: S (and P) of tile t at t * BN, O of tile t behind them
-  static constexpr int kOCol = NT * BN;
+      NT == 2 ? (MODE == kChunkTma ? 168 : 160) : (MODE == kChunkTma ? 152 : 128);
+  static constexpr int kOtherRegs =
+      (kWarps * kLaunchRegs - kSoftmaxWarps * kSoftmaxRegs) / (kWarps - kSoftmaxWarps) / 8 * 8;
+  static_assert(kOtherRegs >= 56, "the split draws on the launch's registers");
+  // TMEM columns: S (and P) of tile t, buffer i at (2 t + i) * BN, O of tile t
+  // behind them
+  static constexpr int kOCol = NT * 2 * BN;
   static constexpr int kColsUsed = kOCol + NT * D;
   static constexpr int kTmemCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
   static_assert(kColsUsed <= 512, "TMEM holds 512 columns");
@@ -164,15 +171,78 @@ struct ChunkCfg {
   // bytes for tiles: 224 KB for one CTA per SM, 111 KB for two
   static constexpr int kBudget = kCtas == 2 ? 111 * 1024 : 224 * 1024;
   static constexpr int kFit = (kBudget - NT * kQTile - kRawStages * kRaw) / kBuf;
-  static constexpr int kBufs = kFit < 8 ? kFit : 8;
+  static constexpr int kBufs = kFit < 10 ? kFit : 10;
   static_assert(kBufs >= 3, "a K and a V step in use and one arriving");
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + NT * kQTile;
   static constexpr int kRawOff = kRing + kBufs * kBuf;
   static constexpr int kBytes = kRawOff + kRawStages * kRaw;
-  static constexpr int kSmall = 256;  // barriers, TMEM address, abort flag
-  static constexpr int kRequest = 1024 + kBytes + kSmall;
+  static constexpr int kSmall = 320;  // barriers, TMEM address, abort flag
+  // (the base is 1024-byte aligned as it is: a block's dynamic shared memory
+  // starts behind 1 KB of the system's; the kernel checks that the slack holds)
+  static constexpr int kSlack = 512;
+  static constexpr int kRequest = kSlack + kBytes + kSmall;
+  static_assert(kRequest <= 227 * 1024, "shared memory of a block");
 };
+
+// mbar_wait_or_abort with little between the polls: the timer and the abort
+// flag are looked at every 32nd time (reading %globaltimer at each poll made
+// a step's hand-overs take longer than its MMAs).
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) == 0) {
+      uint32_t a;
+      asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(a) : "r"(abort));
+      if (a) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        asm volatile("st.volatile.shared.u32 [%0], %1;\n" ::"r"(abort), "r"(1u) : "memory");
+        return false;
+      }
+    }
+  }
+}
+
+// Whether the phase with parity `parity` is over, without waiting. A ready
+// wait takes about 110 clocks from issue to branch; asking early hides them.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// mbar_arrive / mbar_arrive_expect_tx of one lane of a converged warp,
+// predicated (a branch around them takes longer than they do).
+__device__ __forceinline__ void mbar_arrive_by(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred q;\n"
+      "  setp.ne.b32 q, %1, 0;\n"
+      "  @q mbarrier.arrive.shared::cta.b64 _, [%0];\n"
+      "}\n" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_by(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred q;\n"
+      "  setp.ne.b32 q, %2, 0;\n"
+      "  @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+      "}\n" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
 
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;
@@ -195,6 +265,46 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// TMEM store of 16 consecutive 32-bit columns of this warp's lanes.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 2^y of two values on the FMA pipe (the exponential unit, at 4 lanes a clock
+// per scheduler, is as slow as the MMAs): y = n + r with n the nearest whole
+// number, 2^r = 1 + r (c1 + r (c2 + ...)) with coefficients fitted here by
+// minimising the largest relative error over |r| <= 1/2 (degree 3: 1.1e-4, for
+// bf16 weights, whose rounding is 2^-9 at most... degree 4: 2.9e-6, for f16),
+// and n added to the exponent. At or below -127, and for -inf, the result is
+// exactly 0 (the polynomial is exactly 1 at r = 0).
+template <int DEGREE>
+__device__ __forceinline__ float2 exp2_fma(uint64_t y2) {
+  float2 y = unpack_f32x2(y2);
+  y2 = pack_f32x2(fmaxf(y.x, -127.f), fmaxf(y.y, -127.f));
+  const float kRound = 12582912.f;  // 1.5 * 2^23: the sum's low bits are n
+  const uint64_t t2 = add_f32x2(y2, pack_f32x2(kRound, kRound));
+  const uint64_t n2 = add_f32x2(t2, pack_f32x2(-kRound, -kRound));
+  const uint64_t r2 = fma_f32x2(n2, pack_f32x2(-1.f, -1.f), y2);
+  uint64_t p2;
+  if constexpr (DEGREE == 3) {
+    p2 = fma_f32x2(r2, pack_f32x2(0.05500892922f, 0.05500892922f), pack_f32x2(0.24221095443f, 0.24221095443f));
+    p2 = fma_f32x2(p2, r2, pack_f32x2(0.69328290224f, 0.69328290224f));
+  } else {
+    p2 = fma_f32x2(r2, pack_f32x2(0.00958285294f, 0.00958285294f), pack_f32x2(0.05590642616f, 0.05590642616f));
+    p2 = fma_f32x2(p2, r2, pack_f32x2(0.24024099112f, 0.24024099112f));
+    p2 = fma_f32x2(p2, r2, pack_f32x2(0.69312417507f, 0.69312417507f));
+  }
+  p2 = fma_f32x2(p2, r2, pack_f32x2(1.f, 1.f));
+  const float2 p = unpack_f32x2(p2), t = unpack_f32x2(t2);
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
 // The larger of three; NaN if any is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
@@ -212,33 +322,40 @@ __device__ __forceinline__ void set_fewer_regs() {
 
 // Grid: tiles x KV heads x head blocks x partitions, partition fastest, the
 // batch's last tiles first (in a causal chunk they see the most tokens).
-template <typename TQ, int D, int NT, int BN, int MODE>
-__global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
-                                  ChunkCfg<D, NT, BN, MODE>::kCtas)
+template <typename TQ, int D, int NT, int MODE>
+__global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
+                                  ChunkCfg<D, NT, MODE>::kCtas)
     pa_chunk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
-  using C = ChunkCfg<D, NT, BN, MODE>;
+  using C = ChunkCfg<D, NT, MODE>;
   // the operands' type: an E4M3 cache is widened to f16, and q folded into it
   constexpr bool BF16 = MODE != kChunkE4m3 && std::is_same<TQ, __nv_bfloat16>::value;
+  constexpr int BN = C::BN;
   constexpr int SLABS = C::kSlabs;
   constexpr int NBUF = C::kBufs;
   constexpr uint32_t kIdescS = umma_idesc<BF16, BN, false>();
   constexpr uint32_t kIdescPV = umma_idesc<BF16, D, true>();
+  // every kFmaExp-th pair of a row takes its exponentials on the FMA pipe
+  constexpr int kFmaExp = NT == 2 ? PA_CHUNK_FMA_EXP : 0;
 
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t raw = smem_addr(smem);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t small = base + C::kBytes;
-  const uint32_t bar_full = small;            // + 8 * buffer (<= 8)
-  const uint32_t bar_free = small + 64;       // + 8 * buffer
-  const uint32_t bar_s = small + 128;         // + 8 * tile
-  const uint32_t bar_p = small + 144;         // + 8 * tile
-  const uint32_t bar_o = small + 160;         // + 8 * tile
-  const uint32_t bar_q = small + 176;
-  const uint32_t bar_done = small + 184;
-  const uint32_t tmem_slot = small + 192;
-  const uint32_t abort = small + 196;
+  if (base - raw > static_cast<uint32_t>(C::kSlack)) {  // (uniform; never so)
+    if (threadIdx.x == 0) flag_error(PA_DEVERR_TIMEOUT);
+    return;
+  }
+  const uint32_t bar_full = small;            // + 8 * buffer (<= 10)
+  const uint32_t bar_free = small + 80;       // + 8 * buffer
+  const uint32_t bar_s = small + 160;         // + 16 * tile + 8 * S buffer
+  const uint32_t bar_p = small + 192;         // + 16 * tile + 8 * S buffer
+  const uint32_t bar_pv = small + 272;        // + 16 * tile + 8 * S buffer
+  const uint32_t bar_q = small + 240;
+  const uint32_t bar_done = small + 248;
+  const uint32_t tmem_slot = small + 264;
+  const uint32_t abort = small + 268;
   const uint32_t sQ = base + C::kQ;
   const uint32_t sRing = base + C::kRing;
 
@@ -261,7 +378,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
   u /= p.head_blocks;
   const int hk = u % p.num_kv_heads;
   const int x = p.num_tiles - 1 - u / p.num_kv_heads;
-  const ChunkTile ct = chunk_tile(p, x, NT * p.tile_tokens, BN);
+  const ChunkTile ct = chunk_tile(p, x, NT * p.tile_tokens);
   if (ct.b < 0) return;
   const int h0 = hk * p.group + hb * p.head_rows;                 // first query head
   const int heads = min(p.head_rows, p.group - hb * p.head_rows);  // query heads here
@@ -286,18 +403,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  if (tid == C::kMmaWarp * 32) {
+  if (tid == C::kSWarp * 32) {
     for (int i = 0; i < NBUF; ++i) {
       mbar_init(bar_full + 8 * i, MODE == kChunkTma ? 1 : C::kLoadThreads);
-      mbar_init(bar_free + 8 * i, 1);
+      mbar_init(bar_free + 8 * i, NT);
     }
     for (int t = 0; t < NT; ++t) {
-      mbar_init(bar_s + 8 * t, 1);
-      mbar_init(bar_p + 8 * t, 128);
-      mbar_init(bar_o + 8 * t, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar_s + 16 * t + 8 * i, 1);
+        mbar_init(bar_p + 16 * t + 8 * i, 4);
+        mbar_init(bar_pv + 16 * t + 8 * i, 1);
+      }
     }
     mbar_init(bar_q, MODE == kChunkE4m3 ? 128 * NT : 1);
-    mbar_init(bar_done, 1);
+    mbar_init(bar_done, 2 * NT);
     asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(abort), "r"(0u) : "memory");
     mbar_init_fence();
   }
@@ -341,7 +460,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
   // (one register change per group of four warps, at one place)
   if (warp < C::kSoftmaxWarps) {
     set_more_regs<C::kSoftmaxRegs>();
-    // ---- softmax: thread = row ----------------------------------------------------
+    // ---- softmax: thread = row --------------------------------------------------
     const int tile = warp >> 2;
     const int my_row = tid & (kUmmaRows - 1);
     const int my_tok = tile * p.tile_tokens + my_row / p.head_rows;  // within the CTA tile
@@ -349,7 +468,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
     const bool live = my_row < p.tile_tokens * p.head_rows && my_tok < ct.tokens && my_head < heads;
     const bool warp_live = __any_sync(0xffffffffu, live);
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + t_lane + tile * BN;
+    const uint32_t tS = tmem + t_lane + tile * 2 * BN;
     const uint32_t tO = tmem + t_lane + C::kOCol + tile * D;
     const int64_t row = (ct.row + my_tok) * p.num_q_heads + h0 + my_head;
     const int pos = ct.pos0 + my_tok;
@@ -412,38 +531,66 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
     float l_run = 0.f;
     for (int it = a; it < b; ++it) {
       const int j0 = c0 + it * BN;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait_or_abort(bar_s + 8 * tile, static_cast<uint32_t>((it - a) & 1), abort));
+      const uint32_t tSi = tS + ((it - a) & 1) * BN;
+      ok = __all_sync(0xffffffffu, chunk_wait(bar_s + 16 * tile + 8 * ((it - a) & 1),
+                                              static_cast<uint32_t>(((it - a) >> 1) & 1), abort));
       if (!ok) break;
       tc_fence_after();
+      // V rows that no row of the CTA attends: zeros (their blocks may hold
+      // anything). Loader warps have put zeros there.
+      auto zero_v = [&]() -> bool {
+        if constexpr (MODE == kChunkTma) {
+          const int z_hi = c1 - j0, z_lo = ct.lo - j0;
+          if (z_hi < BN || z_lo > 0) {
+            const int n = 2 * it + 1;
+            ok = __all_sync(0xffffffffu,
+                            chunk_wait(bar_full + 8 * (n % NBUF), parity(n), abort));
+            if (!ok) return false;
+            for (int i = my_row; i < BN * SLABS * 8; i += 128) {
+              const int r = i >> 3 & (BN - 1);
+              if (r >= z_hi || r < z_lo)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(buf(n) + i * 16), "r"(0u)
+                             : "memory");
+            }
+            fence_async_smem();
+          }
+        }
+        return true;
+      };
       if (warp_live) {
-        float s[BN];
-#pragma unroll
-        for (int c = 0; c < BN; c += 32) {
-          float h[32];
-          tmem_ld32(tS + c, h);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[c + j] = h[j];
-        }
-        tmem_ld_wait();
-        if (p.sign != 1.f) {  // a negative or zero scale
-#pragma unroll
-          for (int j = 0; j < BN; ++j) s[j] *= p.sign;
-        }
         // tokens this row does not attend
-        if (j0 + BN - 1 > pos_first || (p.window > 0 && j0 <= pos_last - p.window) || j0 + BN > c1) {
-          const int up = min(pos, c1 - 1) - j0;
-          const int dn = first - j0;
+        const bool edge = j0 + BN - 1 > pos_first || (p.window > 0 && j0 <= pos_last - p.window) ||
+                          j0 + BN > c1;
+        const int see_hi = min(pos, c1 - 1) - j0;
+        const int see_lo = first - j0;
+        auto mask32 = [&](int c, float (&h)[32]) {
+          if (p.sign != 1.f) {  // a negative or zero scale
 #pragma unroll
-          for (int j = 0; j < BN; ++j)
-            if (j > up || j < dn) s[j] = -INFINITY;
-        }
-        // the row's maximum in four chains of three-input maxima; NaN if a score is
+            for (int j = 0; j < 32; ++j) h[j] *= p.sign;
+          }
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j > see_hi || c + j < see_lo) h[j] = -INFINITY;
+          }
+        };
+        // the row's maximum: four chains of three-input maxima; NaN if a score is
         float m4[4];
+        auto max32 = [&](const float (&h)[32], bool start) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = max3_nan(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
-#pragma unroll
-        for (int j = 12; j + 1 < BN; j += 2) m4[(j >> 1) & 3] = max3_nan(m4[(j >> 1) & 3], s[j], s[j + 1]);
+          for (int j = 0; j < 32; j += 2) {
+            const int i = (j >> 1) & 3;
+            m4[i] = start && j < 8 ? max3_nan(h[j], h[j + 1], h[j + 1]) : max3_nan(m4[i], h[j], h[j + 1]);
+          }
+        };
+        float s0[32], s1[32];
+        tmem_ld32(tSi, s0);
+        tmem_ld32(tSi + 32, s1);
+        tmem_ld_wait();
+        mask32(0, s0);
+        max32(s0, true);
+        mask32(32, s1);
+        max32(s1, false);
         float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
         mx *= scale_log2;
         const bool up = mx > m_run + kRescaleLog2;  // (the first finite maximum always moves it)
@@ -454,25 +601,39 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
         const uint64_t sc2 = pack_f32x2(scale_log2, scale_log2);
         const uint64_t nm2 = pack_f32x2(neg_m, neg_m);
         uint64_t sum2[2] = {0ull, 0ull};
+        auto exp32 = [&](int c, const float (&h)[32]) {
+          uint32_t pw[16];
 #pragma unroll
-        for (int c = 0; c < BN; c += 64) {
-          uint32_t pw[32];
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(s[c + j], s[c + j + 1]), sc2, nm2));
-            const float p0 = ex2(y.x);
-            const float p1 = ex2(y.y);
-            sum2[(j >> 1) & 1] = add_f32x2(sum2[(j >> 1) & 1], pack_f32x2(p0, p1));
-            pw[j / 2] = pack2<BF16>(p0, p1);
+          for (int j = 0; j < 32; j += 2) {
+            const uint64_t y2 = fma_f32x2(pack_f32x2(h[j], h[j + 1]), sc2, nm2);
+            float2 e2;
+            if (kFmaExp > 0 && (j / 2) % (kFmaExp > 0 ? kFmaExp : 1) == kFmaExp - 1) {
+              e2 = exp2_fma<BF16 ? 3 : 4>(y2);
+            } else {
+              const float2 y = unpack_f32x2(y2);
+              e2 = make_float2(ex2(y.x), ex2(y.y));
+            }
+            sum2[(j >> 1) & 1] = add_f32x2(sum2[(j >> 1) & 1], pack_f32x2(e2.x, e2.y));
+            pw[j / 2] = pack2<BF16>(e2.x, e2.y);
           }
-          tmem_st32u(tS + c / 2, pw);
-        }
+          tmem_st16u(tSi + c / 2, pw);
+        };
+        exp32(0, s0);
+        exp32(32, s1);
         const float2 t2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
         l_run = l_run * alpha + (t2.x + t2.y);
         m_run = m_ref;
-        // rows whose reference maximum moved rescale their O row (the tile's
-        // earlier P.V are done: S(it) was issued behind them)
+        // rows whose reference maximum moved rescale their O row, once P.V(it - 1)
+        // is done (a full S(it) says that P.V(it - 2) is)
         if (it > a && __any_sync(0xffffffffu, up)) {
+          const int n = it - a - 1;
+          ok = __all_sync(0xffffffffu, chunk_wait(bar_pv + 16 * tile + 8 * (n & 1),
+                                                  static_cast<uint32_t>((n >> 1) & 1), abort));
+          if (!ok) {
+            tmem_st_wait();  // (P's store) before the CTA drains
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -485,28 +646,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
         }
         tmem_st_wait();
       }
-      if constexpr (MODE == kChunkTma) {
-        // V rows that no row of the CTA attends: zeros (their blocks may hold anything)
-        const int z_hi = max(c1 - j0, 0), z_lo = ct.lo - j0;
-        if (z_hi < BN || z_lo > 0) {
-          const int n = 2 * it + 1;
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_or_abort(bar_full + 8 * (n % NBUF), parity(n), abort));
-          if (!ok) break;
-          for (int i = my_row; i < BN * SLABS * 8; i += 128) {
-            const int r = i >> 3 & (BN - 1);
-            if (r >= z_hi || r < z_lo)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(buf(n) + i * 16), "r"(0u)
-                           : "memory");
-          }
-          fence_async_smem();
-        }
-      }
+      if (!zero_v()) break;
       tc_fence_before();
-      mbar_arrive(bar_p + 8 * tile);
+      __syncwarp();
+      mbar_arrive_by(lane == 0, bar_p + 16 * tile + 8 * ((it - a) & 1));
     }
-    if (ok && b > a) {
-      ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar_o + 8 * tile, 0u, abort));
+    if (ok && b > a) {  // the last P.V
+      const int n = b - a - 1;
+      ok = __all_sync(0xffffffffu, chunk_wait(bar_pv + 16 * tile + 8 * (n & 1),
+                                              static_cast<uint32_t>((n >> 1) & 1), abort));
       tc_fence_after();
     }
     // ---- the row's result (or its partial) -------------------------------------------
@@ -554,8 +702,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
       if (live && p.num_partitions > 1)
         p.ws_ml[row * p.num_partitions + part] = make_float2(m_run, l_run);
     }
-  } else if (MODE != kChunkTma && warp < C::kMmaWarp) {
-    set_fewer_regs<C::kLoadRegs>();
+  } else if (MODE != kChunkTma && warp < C::kSWarp) {
+    set_fewer_regs<C::kOtherRegs>();
     if constexpr (MODE != kChunkTma) {
       // ---- loader warps: 16-byte pieces with cp.async -------------------------
       const int lt = tid - C::kSoftmaxWarps * 32;
@@ -630,7 +778,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
       const int total = 2 * nsteps;
       if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) load_q();
       auto wait_free = [&](int n) {
-        return n < NBUF || mbar_wait_or_abort(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
+        return n < NBUF || chunk_wait(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
       };
       for (int n = 0; n < total + kAhead; ++n) {
         if (n < total) {
@@ -649,84 +797,86 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
       if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) drain_q();
     }
   } else {
-    set_fewer_regs<C::kMmaRegs>();
-    if (warp == C::kMmaWarp) {
-      // ---- MMA issue --------------------------------------------------------------
-      // MMAs of one thread run in issue order, so S(it + 1) may follow the P.V(it)
-      // that reads P from the same columns, and a full S also says that the
-      // tile's earlier P.V are done.
-      if (lane == 0 && nsteps > 0) {
-        int a[NT], b[NT];
-  #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          a[t] = t < ntiles ? tile_a(t) : 0;
-          b[t] = t < ntiles ? tile_b(t) : 0;
-        }
-        auto full = [&](int n) {
-          return mbar_wait_or_abort(bar_full + 8 * (n % NBUF), parity(n), abort);
-        };
-        auto issue_s = [&](int t, int it) {
-          const uint32_t k = buf(2 * it);
-  #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t ad = sw128_desc(
-                sQ + t * C::kQTile + (kk >> 2) * (kUmmaRows * 128) + (kk & 3) * 32, 16, 1024);
-            const uint64_t bd = sw128_desc(k + (kk >> 2) * C::kBufSlab + (kk & 3) * 32, 16, 1024);
-            umma_f16(tmem + t * BN, ad, bd, kIdescS, kk > 0);
-          }
-          umma_commit(bar_s + 8 * t);
-        };
-        ok = mbar_wait_or_abort(bar_q, 0, abort) && full(0);
-        tc_fence_after();
-        if (ok) {
-  #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            if (a[t] == 0 && b[t] > 0) issue_s(t, 0);
-          umma_commit(bar_free);
-        }
+    set_fewer_regs<C::kOtherRegs>();
+    if (warp >= C::kSWarp && warp < C::kPvWarp + NT) {
+      // ---- MMA issue: per tile one warp for S and one for P.V ------------------
+      // S has two buffers per tile, so that S(it + 1) is there when the softmax
+      // warps finish S(it). A warp needs about 60 clocks to issue an MMA (one of
+      // N = 64 runs in 33 to 49), 110 for a wait and 60 for a commit, so a warp
+      // for everything could not keep the tensor core busy; four can.
+      if (nsteps > 0) {
+        const bool is_s = warp < C::kPvWarp;
+        const int t = (warp - C::kSWarp) % NT;
+        const int a = t < ntiles ? tile_a(t) : 0;
+        const int b = t < ntiles ? tile_b(t) : 0;
+        const uint32_t tS = tmem + t * 2 * BN;
+        const uint32_t tO = tmem + C::kOCol + t * D;
+        // descriptors of Q's tile, and of the ring as K (both slabs K-major) and
+        // as V (MN-major); offsets add in 16-byte units
+        const uint64_t dq = sw128_desc(sQ + t * C::kQTile, 16, 1024);
+        const uint64_t dkv = is_s ? sw128_desc(sRing, 16, 1024) : sw128_desc(sRing, C::kBufSlab, 1024);
+        // ring position: K of step i is buffer 2 i, V 2 i + 1
+        int slot = is_s ? 0 : 1;
+        uint32_t phase = 0;
+        if (is_s) ok = chunk_wait(bar_q, 0, abort);
+        // (a parity wait tells a phase from the one before or after only; so
+        // every barrier here is waited for when its last phase but one is known
+        // to be over and its next cannot end yet. With an odd ring K and V share
+        // slots, and only P.V(it - 2), waited for first, says that V(it - 2) has
+        // been there: no asking ahead.)
+        constexpr bool kAsk = NBUF % 2 == 0;
+        bool ready = false;  // asked ahead whether the buffer is full
         for (int it = 0; ok && it < nsteps; ++it) {
-          const uint32_t v = buf(2 * it + 1);
-          const bool more = it + 1 < nsteps;
-  #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (ok && it >= a[t] && it < b[t]) {
-              ok = mbar_wait_or_abort(bar_p + 8 * t, static_cast<uint32_t>((it - a[t]) & 1), abort) &&
-                   full(2 * it + 1);
-              if (ok) {
-                tc_fence_after();
-  #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  umma_f16_tmem_a(tmem + C::kOCol + t * D, tmem + t * BN + kk * 8,
-                                  sw128_desc(v + kk * 16 * 128, C::kBufSlab, 1024), kIdescPV,
-                                  (it > a[t] || kk > 0) ? 1u : 0u);
-                if (it == b[t] - 1) umma_commit(bar_o + 8 * t);
-              }
-            }
-            if (ok && more && it + 1 >= a[t] && it + 1 < b[t]) {
-              ok = full(2 * it + 2);
-              if (ok) {
-                tc_fence_after();
-                issue_s(t, it + 1);
-              }
-            }
+          const bool mine = it >= a && it < b;
+          const uint32_t i = (it - a) & 1, ph = ((it - a) >> 1) & 1;
+          if (kAsk && !ready) ready = mbar_test(bar_full + 8 * slot, phase);
+          if (mine) {
+            // S: the buffer's last P has been read; P.V: P is there
+            if (is_s)
+              ok = it - a < 2 || chunk_wait(bar_pv + 16 * t + 8 * i, ph ^ 1, abort);
+            else
+              ok = chunk_wait(bar_p + 16 * t + 8 * i, ph, abort);
           }
-          if (!ok || !full(2 * it + 1)) break;
-          umma_commit(bar_free + 8 * ((2 * it + 1) % NBUF));
-          if (more) {
-            if (!full(2 * it + 2)) break;
-            umma_commit(bar_free + 8 * ((2 * it + 2) % NBUF));
+          if (!ok || !(ok = ready || chunk_wait(bar_full + 8 * slot, phase, abort))) break;
+          const uint32_t free_bar = bar_free + 8 * slot;
+          const uint64_t dst = dkv + static_cast<uint32_t>(slot * (C::kBuf >> 4));
+          slot += 2;
+          if (slot >= NBUF) {
+            slot -= NBUF;
+            phase ^= 1;
           }
+          tc_fence_after();
+          if (lane == 0) {
+            if (mine && is_s) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_f16(tS + i * BN, dq + (((kk >> 2) * (kUmmaRows * 128) + (kk & 3) * 32) >> 4),
+                         dst + (((kk >> 2) * C::kBufSlab + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
+              umma_commit(bar_s + 16 * t + 8 * i);
+            } else if (mine) {
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                umma_f16_tmem_a(tO, tS + i * BN + kk * 8, dst + (kk * 16 * 128 >> 4), kIdescPV,
+                                (it > a || kk > 0) ? 1u : 0u);
+              umma_commit(bar_pv + 16 * t + 8 * i);
+            }
+            umma_commit(free_bar);
+          }
+          __syncwarp();
+          ready = kAsk && it + 1 < nsteps && mbar_test(bar_full + 8 * slot, phase);
         }
         // every issued MMA has completed before TMEM is released
-        umma_commit(bar_done);
+        if (lane == 0) umma_commit(bar_done);
+        __syncwarp();
         mbar_wait(bar_done, 0);
       }
-    } else if (MODE == kChunkTma && warp == C::kSoftmaxWarps) {
-      // ---- TMA producer: lane i issues box (unit i / SLABS, slab i % SLABS) ----
-      if (lane == 0) {
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
-      }
+    } else if (MODE == kChunkTma && warp < C::kSWarp) {
+      // ---- TMA producers (K, and V): lane i issues box (unit i / SLABS, slab
+      // i % SLABS) of each step
+      const int kv = warp - C::kSoftmaxWarps;
+      const CUtensorMap* map = kv ? &tm_v : &tm_k;
+      if (lane == 0)
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
       const int bs_mask = (1 << p.bs_log2) - 1;
       const int unit = min(1 << p.bs_log2, BN);
       const int nbox = BN / unit * SLABS;  // <= 32
@@ -741,35 +891,29 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
         const int blk = block_of(j);
         return blk < 0 ? p.num_slots : (blk << p.bs_log2) + (j & bs_mask);
       };
-      auto load = [&](const CUtensorMap* map, int n, int slot) {
+      if (kv == 0) load_q();
+      int issued = 0;  // steps
+      int slot = nsteps > 0 ? slot_of(0) : 0;
+      for (int it = 0; it < nsteps; ++it) {
+        const int next = it + 1 < nsteps ? slot_of(it + 1) : 0;
+        const int n = 2 * it + kv;
+        if (n >= NBUF && !__all_sync(0xffffffffu, chunk_wait(bar_free + 8 * (n % NBUF),
+                                                              parity(n - NBUF), abort)))
+          break;
         const uint32_t bar = bar_full + 8 * (n % NBUF);
-        if (lane == 0) mbar_arrive_expect_tx(bar, C::kBuf);
+        mbar_arrive_expect_tx_by(lane == 0, bar, C::kBuf);
         __syncwarp();
         if (lane < nbox) tma_load_3d(buf(n) + sl * C::kBufSlab + u0 * 128, map, bar, sl * 64, hk, slot);
-      };
-      load_q();
-      int issued = 0;
-      int slot = nsteps > 0 ? slot_of(0) : 0;
-      for (int it = 0; it < nsteps && ok; ++it) {
-        const int next = it + 1 < nsteps ? slot_of(it + 1) : 0;
-        for (int n = 2 * it; n < 2 * it + 2; ++n) {
-          if (n >= NBUF &&
-              !__all_sync(0xffffffffu, mbar_wait_or_abort(bar_free + 8 * (n % NBUF),
-                                                          parity(n - NBUF), abort))) {
-            ok = false;
-            break;
-          }
-          load((n & 1) ? &tm_v : &tm_k, n, slot);
-          issued = n + 1;
-        }
+        issued = it + 1;
         slot = next;
       }
-      // every issued copy has landed before the CTA can exit
-      if (lane == 0) {
-        for (int n = max(issued - NBUF, 0); n < issued; ++n)
-          mbar_wait(bar_full + 8 * (n % NBUF), parity(n));
-      }
-      drain_q();
+      // every issued copy has landed before the CTA can exit: those of the last
+      // NBUF buffers (an earlier one's barrier has gone on to a later buffer)
+      if (lane == 0)
+        for (int it = max(issued - (NBUF + 1) / 2, 0); it < issued; ++it)
+          if (2 * it + kv >= 2 * issued - NBUF)
+            mbar_wait(bar_full + 8 * ((2 * it + kv) % NBUF), parity(2 * it + kv));
+      if (kv == 0) drain_q();
     }
   }
 
@@ -788,12 +932,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, BN, MODE>::kThreads,
 // partials that the attention kernel wrote (the tile's own token range says
 // how many), weighted by l 2^(m - max m).
 template <typename TQ, int D>
-__global__ void __launch_bounds__(256) pa_chunk_merge_kernel(const ChunkParams p, int cta_tokens,
-                                                             int step) {
+__global__ void __launch_bounds__(256) pa_chunk_merge_kernel(const ChunkParams p, int cta_tokens) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const ChunkTile ct = chunk_tile(p, blockIdx.x, cta_tokens, step);
+  const ChunkTile ct = chunk_tile(p, blockIdx.x, cta_tokens);
   if (ct.b < 0) return;
   const int r = blockIdx.y * 8 + warp;  // row of the tile: (token, query head)
   if (r >= ct.tokens * p.num_q_heads) return;
