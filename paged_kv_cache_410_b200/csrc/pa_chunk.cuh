@@ -129,10 +129,6 @@ constexpr int kChunkTma = 0;     // TMA boxes (16-bit, blocks >= 8)
 constexpr int kChunkCopy = 1;    // cp.async (16-bit, smaller blocks)
 constexpr int kChunkE4m3 = 2;    // cp.async of codes, widened to f16
 
-#ifndef PA_CHUNK_FMA_EXP
-#define PA_CHUNK_FMA_EXP 4
-#endif
-
 template <int D, int NT, int MODE>
 struct ChunkCfg {
   static constexpr int BN = kChunkStep;
@@ -166,10 +162,11 @@ struct ChunkCfg {
   static constexpr int kQTile = kSlabs * kUmmaRows * 128;
   static constexpr int kBufSlab = BN * 128;
   static constexpr int kBuf = kSlabs * kBufSlab;  // one K or V step, 16-bit
-  static constexpr int kRaw = MODE == kChunkE4m3 ? kBuf / 2 : 0;  // its E4M3 codes
-  static constexpr int kRawStages = MODE == kChunkE4m3 ? (NT == 1 ? 3 : 4) : 0;
-  // bytes for tiles: 224 KB for one CTA per SM, 111 KB for two
-  static constexpr int kBudget = kCtas == 2 ? 111 * 1024 : 224 * 1024;
+  // E4M3: the codes of a K and a V step arrive in a raw stage first
+  static constexpr int kRaw = MODE == kChunkE4m3 ? kBuf : 0;
+  static constexpr int kRawStages = MODE == kChunkE4m3 ? (NT == 1 ? 2 : 4) : 0;
+  // bytes for tiles: 224 KB for one CTA per SM, 112 KB for two
+  static constexpr int kBudget = kCtas == 2 ? 112 * 1024 : 224 * 1024;
   static constexpr int kFit = (kBudget - NT * kQTile - kRawStages * kRaw) / kBuf;
   static constexpr int kBufs = kFit < 10 ? kFit : 10;
   static_assert(kBufs >= 3, "a K and a V step in use and one arriving");
@@ -177,7 +174,7 @@ struct ChunkCfg {
   static constexpr int kRing = kQ + NT * kQTile;
   static constexpr int kRawOff = kRing + kBufs * kBuf;
   static constexpr int kBytes = kRawOff + kRawStages * kRaw;
-  static constexpr int kSmall = 320;  // barriers, TMEM address, abort flag
+  static constexpr int kSmall = 336;  // barriers, TMEM address, abort flag
   // (the base is 1024-byte aligned as it is: a block's dynamic shared memory
   // starts behind 1 KB of the system's; the kernel checks that the slack holds)
   static constexpr int kSlack = 512;
@@ -275,42 +272,7 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[1
       : "memory");
 }
 
-// 2^y of two values on the FMA pipe (the exponential unit, at 4 lanes a clock
-// per scheduler, is as slow as the MMAs): y = n + r with n the nearest whole
-// number, 2^r = 1 + r (c1 + r (c2 + ...)) with coefficients fitted here by
-// minimising the largest relative error over |r| <= 1/2 (degree 3: 1.1e-4, for
-// bf16 weights, whose rounding is 2^-9 at most... degree 4: 2.9e-6, for f16),
-// and n added to the exponent. At or below -127, and for -inf, the result is
-// exactly 0 (the polynomial is exactly 1 at r = 0).
-template <int DEGREE>
-__device__ __forceinline__ float2 exp2_fma(uint64_t y2) {
-  float2 y = unpack_f32x2(y2);
-  y2 = pack_f32x2(fmaxf(y.x, -127.f), fmaxf(y.y, -127.f));
-  const float kRound = 12582912.f;  // 1.5 * 2^23: the sum's low bits are n
-  const uint64_t t2 = add_f32x2(y2, pack_f32x2(kRound, kRound));
-  const uint64_t n2 = add_f32x2(t2, pack_f32x2(-kRound, -kRound));
-  const uint64_t r2 = fma_f32x2(n2, pack_f32x2(-1.f, -1.f), y2);
-  uint64_t p2;
-  if constexpr (DEGREE == 3) {
-    p2 = fma_f32x2(r2, pack_f32x2(0.05500892922f, 0.05500892922f), pack_f32x2(0.24221095443f, 0.24221095443f));
-    p2 = fma_f32x2(p2, r2, pack_f32x2(0.69328290224f, 0.69328290224f));
-  } else {
-    p2 = fma_f32x2(r2, pack_f32x2(0.00958285294f, 0.00958285294f), pack_f32x2(0.05590642616f, 0.05590642616f));
-    p2 = fma_f32x2(p2, r2, pack_f32x2(0.24024099112f, 0.24024099112f));
-    p2 = fma_f32x2(p2, r2, pack_f32x2(0.69312417507f, 0.69312417507f));
-  }
-  p2 = fma_f32x2(p2, r2, pack_f32x2(1.f, 1.f));
-  const float2 p = unpack_f32x2(p2), t = unpack_f32x2(t2);
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
-}
-
-// The larger of three; NaN if any is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 template <int N>
 __device__ __forceinline__ void set_more_regs() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -336,8 +298,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   constexpr int NBUF = C::kBufs;
   constexpr uint32_t kIdescS = umma_idesc<BF16, BN, false>();
   constexpr uint32_t kIdescPV = umma_idesc<BF16, D, true>();
-  // every kFmaExp-th pair of a row takes its exponentials on the FMA pipe
-  constexpr int kFmaExp = NT == 2 ? PA_CHUNK_FMA_EXP : 0;
 
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t raw = smem_addr(smem);
@@ -352,6 +312,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   const uint32_t bar_s = small + 160;         // + 16 * tile + 8 * S buffer
   const uint32_t bar_p = small + 192;         // + 16 * tile + 8 * S buffer
   const uint32_t bar_pv = small + 272;        // + 16 * tile + 8 * S buffer
+  const uint32_t s_live = small + 304;        // + 4 * softmax warp: whether it has rows
   const uint32_t bar_q = small + 240;
   const uint32_t bar_done = small + 248;
   const uint32_t tmem_slot = small + 264;
@@ -403,9 +364,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  // the row of a softmax thread: token (within the CTA tile) and query head
+  const int tile = warp >> 2;
+  const int my_row = tid & (kUmmaRows - 1);
+  const int my_tok = tile * p.tile_tokens + my_row / p.head_rows;
+  const int my_head = my_row % p.head_rows;
+  const bool live = warp < C::kSoftmaxWarps && my_row < p.tile_tokens * p.head_rows &&
+                    my_tok < ct.tokens && my_head < heads;
+  const bool warp_live = __any_sync(0xffffffffu, live);
+  if (NT == 2 && lane == 0 && warp < C::kSoftmaxWarps)
+    asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(s_live + 4 * warp), "r"(warp_live ? 1u : 0u) : "memory");
   if (tid == C::kSWarp * 32) {
     for (int i = 0; i < NBUF; ++i) {
-      mbar_init(bar_full + 8 * i, MODE == kChunkTma ? 1 : C::kLoadThreads);
+      mbar_init(bar_full + 8 * i, MODE == kChunkTma ? 1 : C::kLoadWarps);
       mbar_init(bar_free + 8 * i, NT);
     }
     for (int t = 0; t < NT; ++t) {
@@ -461,12 +432,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   if (warp < C::kSoftmaxWarps) {
     set_more_regs<C::kSoftmaxRegs>();
     // ---- softmax: thread = row --------------------------------------------------
-    const int tile = warp >> 2;
-    const int my_row = tid & (kUmmaRows - 1);
-    const int my_tok = tile * p.tile_tokens + my_row / p.head_rows;  // within the CTA tile
-    const int my_head = my_row % p.head_rows;
-    const bool live = my_row < p.tile_tokens * p.head_rows && my_tok < ct.tokens && my_head < heads;
-    const bool warp_live = __any_sync(0xffffffffu, live);
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + t_lane + tile * 2 * BN;
     const uint32_t tO = tmem + t_lane + C::kOCol + tile * D;
@@ -529,6 +494,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
     const int pos_last = ct.pos0 + min((tile + 1) * p.tile_tokens, ct.tokens) - 1;
     float m_run = -INFINITY;
     float l_run = 0.f;
+    // Turns of the exponential unit: warp w of tile 0 and warp w of tile 1 sit on
+    // the same scheduler. In step they would use each pipe at the same time and
+    // leave the others idle; in turn one computes its exponentials while the
+    // other loads its scores, finds their maximum and stores P. Steps that both
+    // tiles have, where both warps have rows; tile 0 starts. A warp that gives up
+    // hands the turn on once, and the other sees the abort flag before it waits
+    // for another.
+    int turn_a = 0, turn_b = 0;
+    const int my_turn = 1 + tile * 4 + (warp & 3), other_turn = 1 + (tile ^ 1) * 4 + (warp & 3);
+    if constexpr (NT == 2) {
+      uint32_t other;
+      asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(other) : "r"(s_live + 4 * (warp ^ 4)));
+      if (ntiles == 2 && warp_live && other) {
+        turn_a = max(tile_a(0), tile_a(1));
+        turn_b = min(tile_b(0), tile_b(1));
+        if (tile == 1 && turn_a < turn_b)
+          asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
+      }
+    }
     for (int it = a; it < b; ++it) {
       const int j0 = c0 + it * BN;
       const uint32_t tSi = tS + ((it - a) & 1) * BN;
@@ -574,13 +558,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
               if (c + j > see_hi || c + j < see_lo) h[j] = -INFINITY;
           }
         };
-        // the row's maximum: four chains of three-input maxima; NaN if a score is
+        // the row's maximum: four chains of three-input maxima (a NaN score is
+        // passed over here and makes its weight, and so the row, NaN below)
         float m4[4];
         auto max32 = [&](const float (&h)[32], bool start) {
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             const int i = (j >> 1) & 3;
-            m4[i] = start && j < 8 ? max3_nan(h[j], h[j + 1], h[j + 1]) : max3_nan(m4[i], h[j], h[j + 1]);
+            m4[i] = start && j < 8 ? max3(h[j], h[j + 1], h[j + 1]) : max3(m4[i], h[j], h[j + 1]);
           }
         };
         float s0[32], s1[32];
@@ -591,13 +576,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
         max32(s0, true);
         mask32(32, s1);
         max32(s1, false);
-        float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+        float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]);
         mx *= scale_log2;
         const bool up = mx > m_run + kRescaleLog2;  // (the first finite maximum always moves it)
         const float m_ref = up ? mx : m_run;
         const float alpha = up ? ex2(m_run - m_ref) : 1.f;
         // a row that has seen no token yet keeps p = 2^(-inf) = 0
-        const float neg_m = mx != mx ? mx : m_ref == -INFINITY ? 0.f : -m_ref;
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t sc2 = pack_f32x2(scale_log2, scale_log2);
         const uint64_t nm2 = pack_f32x2(neg_m, neg_m);
         uint64_t sum2[2] = {0ull, 0ull};
@@ -606,20 +591,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             const uint64_t y2 = fma_f32x2(pack_f32x2(h[j], h[j + 1]), sc2, nm2);
-            float2 e2;
-            if (kFmaExp > 0 && (j / 2) % (kFmaExp > 0 ? kFmaExp : 1) == kFmaExp - 1) {
-              e2 = exp2_fma<BF16 ? 3 : 4>(y2);
-            } else {
-              const float2 y = unpack_f32x2(y2);
-              e2 = make_float2(ex2(y.x), ex2(y.y));
-            }
+            const float2 y = unpack_f32x2(y2);
+            const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
             sum2[(j >> 1) & 1] = add_f32x2(sum2[(j >> 1) & 1], pack_f32x2(e2.x, e2.y));
             pw[j / 2] = pack2<BF16>(e2.x, e2.y);
           }
           tmem_st16u(tSi + c / 2, pw);
         };
+        // the exponentials of the two tiles' warps of one scheduler take turns
+        const bool turn = it >= turn_a && it < turn_b;
+        if (turn) {
+          uint32_t gone;
+          asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort));
+          if (gone) {
+            ok = false;
+            break;
+          }
+          asm volatile("bar.sync %0, 64;\n" ::"r"(my_turn) : "memory");
+        }
         exp32(0, s0);
         exp32(32, s1);
+        if (turn && (tile == 0 || it + 1 < turn_b))
+          asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
         const float2 t2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
         l_run = l_run * alpha + (t2.x + t2.y);
         m_run = m_ref;
@@ -651,6 +644,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
       __syncwarp();
       mbar_arrive_by(lane == 0, bar_p + 16 * tile + 8 * ((it - a) & 1));
     }
+    if (!ok && turn_a < turn_b) asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
     if (ok && b > a) {  // the last P.V
       const int n = b - a - 1;
       ok = __all_sync(0xffffffffu, chunk_wait(bar_pv + 16 * tile + 8 * (n & 1),
@@ -713,84 +707,96 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
       static_assert(kPer * C::kLoadThreads == BN * kPieces, "whole rounds");
       const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D * kElem;
       const uint32_t sRaw = base + C::kRawOff;
-      // start the copies of ring buffer n (into the raw stage, or the buffer
-      // itself); tokens outside [lo, c1) and bad blocks become zeros
-      auto start = [&](int n) {
-        const char* cache = reinterpret_cast<const char*>((n & 1) ? p.v_cache : p.k_cache);
-        int64_t slot[kPer];
+      // block of each of this thread's rows of step `it`: -1 for tokens outside
+      // [lo, c1) and bad blocks, which become zeros
+      auto lookup = [&](int it, int (&id)[kPer]) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-          const int j = c0 + (n >> 1) * BN + (lt + k * C::kLoadThreads) / kPieces;
-          slot[k] = -1;
-          if (j >= ct.lo && j < c1) {
-            const int blk = block_of(j);
-            if (blk >= 0)
-              slot[k] = (static_cast<int64_t>(blk) << p.bs_log2) + (j & ((1 << p.bs_log2) - 1));
-          }
+          const int j = c0 + it * BN + (lt + k * C::kLoadThreads) / kPieces;
+          id[k] = j >= ct.lo && j < c1 ? block_of(j) : -1;
         }
+      };
+      // start the copies of a step's K and V (into the raw stage, or the ring
+      // buffers themselves)
+      auto start = [&](int it, const int (&id)[kPer]) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
           const int piece = lt + k * C::kLoadThreads;
           const int r = piece / kPieces, c = piece % kPieces;
-          const char* src = slot[k] < 0 ? cache : cache + slot[k] * row_bytes + hk * (D * kElem) + c * 16;
-          uint32_t dst;
-          if constexpr (MODE == kChunkE4m3)
-            dst = sRaw + (n % C::kRawStages) * C::kRaw + piece * 16;
-          else
-            dst = buf(n) + (c >> 3) * C::kBufSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          cp_async_16(dst, src, slot[k] < 0 ? 0u : 16u);
-        }
-      };
-      // finish buffer n: its copies (this thread's own) have landed
-      auto finish = [&](int n) {
-        if constexpr (MODE == kChunkE4m3) {
+          const int j = c0 + it * BN + r;
+          const int64_t at = ((static_cast<int64_t>(max(id[k], 0)) << p.bs_log2) + (j & ((1 << p.bs_log2) - 1))) *
+                                 row_bytes + hk * (D * kElem) + c * 16;
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int piece = lt + k * C::kLoadThreads;
-            const int r = piece / kPieces, c = piece % kPieces;
-            const uint4 w = lds128(sRaw + (n % C::kRawStages) * C::kRaw + piece * 16);
-            uint4 h[2];
-            e4m3x4_to_f16x2x2(w.x, h[0].x, h[0].y);
-            e4m3x4_to_f16x2x2(w.y, h[0].z, h[0].w);
-            e4m3x4_to_f16x2x2(w.z, h[1].x, h[1].y);
-            e4m3x4_to_f16x2x2(w.w, h[1].z, h[1].w);
-            // the row's two slabs would meet in the same banks: the upper
-            // slab's threads store their odd half first
-            const bool odd = c >= 4;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int half = e ^ (odd ? 1 : 0);
-              const int cc = 2 * c + half;
-              const uint4 v = half ? h[1] : h[0];
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(
-                               buf(n) + (cc >> 3) * C::kBufSlab + r * 128 +
-                               (((cc & 7) ^ (r & 7)) << 4)),
-                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                           : "memory");
-            }
+          for (int kv = 0; kv < 2; ++kv) {
+            const char* cache = reinterpret_cast<const char*>(kv ? p.v_cache : p.k_cache);
+            uint32_t dst;
+            if constexpr (MODE == kChunkE4m3)
+              dst = sRaw + (it % C::kRawStages) * C::kRaw + kv * (C::kRaw / 2) + piece * 16;
+            else
+              dst = buf(2 * it + kv) + (c >> 3) * C::kBufSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            cp_async_16(dst, id[k] < 0 ? cache : cache + at, id[k] < 0 ? 0u : 16u);
           }
         }
-        fence_async_smem();
-        mbar_arrive(bar_full + 8 * (n % NBUF));
       };
-      // copies run kAhead buffers ahead of their use
-      constexpr int kAhead = MODE == kChunkE4m3 ? C::kRawStages - 1 : NBUF - 2;
-      const int total = 2 * nsteps;
-      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) load_q();
       auto wait_free = [&](int n) {
         return n < NBUF || chunk_wait(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
       };
-      for (int n = 0; n < total + kAhead; ++n) {
-        if (n < total) {
-          if (MODE == kChunkCopy && !wait_free(n)) break;
-          start(n);
+      // finish a step whose copies (this thread's own) have landed
+      auto finish = [&](int it) -> bool {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int n = 2 * it + kv;
+          if constexpr (MODE == kChunkE4m3) {
+            uint4 w[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+              w[k] = lds128(sRaw + (it % C::kRawStages) * C::kRaw + kv * (C::kRaw / 2) +
+                            (lt + k * C::kLoadThreads) * 16);
+            if (!wait_free(n)) return false;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const int piece = lt + k * C::kLoadThreads;
+              const int r = piece / kPieces, c = piece % kPieces;
+              uint4 h[2];
+              e4m3x4_to_f16x2x2(w[k].x, h[0].x, h[0].y);
+              e4m3x4_to_f16x2x2(w[k].y, h[0].z, h[0].w);
+              e4m3x4_to_f16x2x2(w[k].z, h[1].x, h[1].y);
+              e4m3x4_to_f16x2x2(w[k].w, h[1].z, h[1].w);
+              // the row's two slabs would meet in the same banks: the upper
+              // slab's threads store their odd half first
+              const bool odd = c >= 4;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int cc = 2 * c + (e ^ (odd ? 1 : 0));
+                const uint4 v = (e ^ (odd ? 1 : 0)) ? h[1] : h[0];
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                                 buf(n) + (cc >> 3) * C::kBufSlab + r * 128 + (((cc & 7) ^ (r & 7)) << 4)),
+                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+              }
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          mbar_arrive_by(lane == 0, bar_full + 8 * (n % NBUF));
+        }
+        return true;
+      };
+      // copies run kAhead steps ahead of their use, table entries one more
+      constexpr int kAhead = MODE == kChunkE4m3 ? C::kRawStages - 1 : NBUF / 2 - 1;
+      if (MODE == kChunkCopy && warp == C::kSoftmaxWarps) load_q();
+      int id[kPer];
+      if (nsteps > 0) lookup(0, id);
+      for (int n = 0; n < nsteps + kAhead; ++n) {
+        if (n < nsteps) {
+          if (MODE == kChunkCopy && !(wait_free(2 * n) && wait_free(2 * n + 1))) break;
+          start(n, id);
+          if (n + 1 < nsteps) lookup(n + 1, id);
         }
         cp_async_commit();
-        const int m = n - kAhead;
-        if (m >= 0) {
+        if (n >= kAhead) {
           cp_async_wait<kAhead>();
-          if (MODE == kChunkE4m3 && !wait_free(m)) break;
-          finish(m);
+          if (!finish(n - kAhead)) break;
         }
       }
       cp_async_wait<0>();
@@ -830,6 +836,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           const bool mine = it >= a && it < b;
           const uint32_t i = (it - a) & 1, ph = ((it - a) >> 1) & 1;
           if (kAsk && !ready) ready = mbar_test(bar_full + 8 * slot, phase);
+          if (kAsk && is_s && !(ok = ready || chunk_wait(bar_full + 8 * slot, phase, abort))) break;
+          ready = ready || (kAsk && is_s);
           if (mine) {
             // S: the buffer's last P has been read; P.V: P is there
             if (is_s)
