@@ -920,6 +920,41 @@ pa_status launch_chunk(const pa::ChunkParams& p, const ChunkPlan& pl, const pa_c
                             : launch_chunk_m<TQ, 128, pa::kChunkCopy>(p, pl, st);
 }
 
+// ---- draft verification ---------------------------------------------------------
+// CTAs per sequence: as many as keep the batch within one wave (two CTAs of
+// 512 threads per SM). At 256 sequences of 131072 tokens eight CTAs each (7
+// waves, each with its own chain of dependent loads) took 131 us.
+template <typename T, bool VEC, int CL>
+pa_status launch_verify_c(const pa::VerifyParams& p, int batch, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch) * CL);
+  cfg.blockDim = dim3(pa::kVerifyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, pa::pa_verify_kernel<T, VEC, CL>, p) == cudaSuccess ? PA_OK
+                                                                                     : PA_ERR_CUDA;
+}
+
+template <typename T, bool VEC>
+pa_status launch_verify_v(const pa::VerifyParams& p, int batch, cudaStream_t st) {
+  const int64_t slots = 2 * kNumSMs;
+  if (int64_t{8} * batch <= slots) return launch_verify_c<T, VEC, 8>(p, batch, st);
+  if (int64_t{4} * batch <= slots) return launch_verify_c<T, VEC, 4>(p, batch, st);
+  if (int64_t{2} * batch <= slots) return launch_verify_c<T, VEC, 2>(p, batch, st);
+  return launch_verify_c<T, VEC, 1>(p, batch, st);
+}
+
+template <typename T>
+pa_status launch_verify_t(const pa::VerifyParams& p, int batch, bool vec, cudaStream_t st) {
+  return vec ? launch_verify_v<T, true>(p, batch, st) : launch_verify_v<T, false>(p, batch, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1064,7 +1099,7 @@ pa_status pa_verify_draft(const int32_t* draft_tokens, int64_t num_drafts, int32
   if (!cu_drafts || !target_probs || !sample_uniforms || !accepted || !tokens ||
       (num_drafts > 0 && (!draft_tokens || !accept_uniforms)))
     return PA_ERR_INVALID_ARG;
-  if (num_drafts > 0x7fffffffLL || batch > 0x7fffffff / pa::kVerifyCtas ||
+  if (num_drafts > 0x7fffffffLL || batch > 0x7fffffff / pa::kVerifyMaxCtas ||
       max_drafts == 0x7fffffff)
     return PA_ERR_UNSUPPORTED;
   const int64_t size = prob_dtype == PA_F32 ? 4 : 2;
@@ -1085,17 +1120,9 @@ pa_status pa_verify_draft(const int32_t* draft_tokens, int64_t num_drafts, int32
   p.max_drafts = max_drafts;
   const bool vec = addr % 16 == 0 && vocab * size % 16 == 0;
   const cudaStream_t s = as_stream(stream);
-  const unsigned grid = static_cast<unsigned>(batch) * pa::kVerifyCtas;
-  auto go = [&](auto kern) {
-    kern<<<grid, pa::kVerifyThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-  };
-  if (prob_dtype == PA_F32)
-    return vec ? go(pa::pa_verify_kernel<float, true>) : go(pa::pa_verify_kernel<float, false>);
-  if (prob_dtype == PA_F16)
-    return vec ? go(pa::pa_verify_kernel<__half, true>) : go(pa::pa_verify_kernel<__half, false>);
-  return vec ? go(pa::pa_verify_kernel<__nv_bfloat16, true>)
-             : go(pa::pa_verify_kernel<__nv_bfloat16, false>);
+  if (prob_dtype == PA_F32) return launch_verify_t<float>(p, batch, vec, s);
+  if (prob_dtype == PA_F16) return launch_verify_t<__half>(p, batch, vec, s);
+  return launch_verify_t<__nv_bfloat16>(p, batch, vec, s);
 }
 
 pa_status pa_calibrate_kv(const void* k, const void* v, int32_t in_dtype, int64_t num_tokens,
@@ -1122,8 +1149,8 @@ pa_status pa_calibrate_kv(const void* k, const void* v, int32_t in_dtype, int64_
   const int width = std::min(groups, 256);
   const int col_blocks = (groups + width - 1) / width;
   const int rows = 256 / width;
-  // four CTAs per SM, at least 16 tokens for each of a CTA's threads
-  const int64_t want = std::max<int64_t>(1, 4 * kNumSMs / (2 * col_blocks));
+  // six CTAs per SM, at least 16 tokens for each of a CTA's threads
+  const int64_t want = std::max<int64_t>(1, 6 * kNumSMs / (2 * col_blocks));
   const int64_t splits = std::max<int64_t>(
       1, std::min<int64_t>(want, num_tokens / (16 * rows)));
   p.tokens_per_split = std::max<int64_t>(1, (num_tokens + splits - 1) / splits);

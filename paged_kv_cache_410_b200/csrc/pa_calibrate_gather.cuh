@@ -56,15 +56,29 @@ __global__ void __launch_bounds__(256) pa_calibrate_kernel(const CalibrateParams
   uint4 m = make_uint4(kBias, kBias, kBias, kBias);  // |x| = 0
   if (r < rows && cg < groups) {
     const uint4* x = reinterpret_cast<const uint4*>(p.x[which]) + cg;
-#pragma unroll 8
-    for (int64_t t = t0 + r; t < t1; t += rows) {
-      const uint4 v = __ldg(x + t * groups);
-      const uint32_t live = p.slots && __ldg(p.slots + t) < 0 ? 0u : 0x7fff7fffu;
+    auto take = [&](const uint4& v, uint32_t live) {
       m.x = __vmaxs2(m.x, (v.x & live) + kBias);
       m.y = __vmaxs2(m.y, (v.y & live) + kBias);
       m.z = __vmaxs2(m.z, (v.z & live) + kBias);
       m.w = __vmaxs2(m.w, (v.w & live) + kBias);
+    };
+    // kBatch tokens' loads in flight at a time (with the slots read in the same
+    // loop the compiler waited for each)
+    constexpr int kBatch = 8;
+    const int64_t step = static_cast<int64_t>(rows) * kBatch;
+    int64_t t = t0 + r;
+    for (; t + step - rows < t1; t += step) {
+      uint4 v[kBatch];
+      int64_t s[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) v[k] = __ldg(x + (t + k * rows) * groups);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) s[k] = p.slots ? __ldg(p.slots + t + k * rows) : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) take(v[k], s[k] < 0 ? 0u : 0x7fff7fffu);
     }
+    for (; t < t1; t += rows)
+      take(__ldg(x + t * groups), p.slots && __ldg(p.slots + t) < 0 ? 0u : 0x7fff7fffu);
   }
   part[threadIdx.x] = m;
   __syncthreads();
