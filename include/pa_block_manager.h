@@ -91,6 +91,28 @@ int32_t pa_bm_append_token(pa_block_manager* bm, int64_t seq_id, int32_t token, 
 int32_t pa_bm_append_tokens(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* tokens,
                             int32_t n, int64_t* slots, int32_t* cow_pairs, int32_t* num_pairs);
 
+/* pa_bm_append_token for runs of tokens: counts[i] >= 0 new tokens for each
+ * of the n distinct sequences seq_ids[i] (a prompt chunk, or the drafts of a
+ * speculative step), their ids one run after the other in `tokens`, their
+ * slots likewise to `slots` (room for the counts' sum). Copy-on-write pairs
+ * (at most one per sequence) as in pa_bm_append_tokens; all blocks are taken
+ * before any token joins the prefix cache. offer == 0 keeps the full blocks
+ * of these tokens out of the prefix cache until pa_bm_keep: drafts that may
+ * be refused. PA_BM_ERR_INVALID for an unknown or repeated id, a negative
+ * count or a length past 2^31 - 1, PA_BM_ERR_NO_BLOCKS if the pool cannot
+ * supply the batch, PA_BM_ERR_CAPACITY if the host is out of memory; either
+ * way nothing has changed. */
+int32_t pa_bm_append_chunks(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* counts,
+                            int32_t n, const int32_t* tokens, int32_t offer, int64_t* slots,
+                            int32_t* cow_pairs, int32_t* num_pairs);
+
+/* Keep the first lengths[i] tokens of each of n distinct sequences and drop
+ * the others (refused drafts): blocks behind them are released, and the full
+ * blocks kept are offered to the prefix cache. A length above the sequence's
+ * or inside blocks already released (sliding window) is PA_BM_ERR_INVALID;
+ * then nothing has changed. */
+int32_t pa_bm_keep(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* lengths, int32_t n);
+
 /* child_id starts as a copy of parent_id that shares all its blocks. */
 int32_t pa_bm_fork(pa_block_manager* bm, int64_t parent_id, int64_t child_id);
 

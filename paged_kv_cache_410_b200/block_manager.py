@@ -14,7 +14,7 @@ EXPORTED = ["pa_bm_create", "pa_bm_destroy", "pa_bm_num_free_blocks", "pa_bm_num
             "pa_bm_block_refcount", "pa_bm_add_sequence", "pa_bm_append_token", "pa_bm_fork",
             "pa_bm_free_sequence", "pa_bm_release_before", "pa_bm_sequence_length",
             "pa_bm_slots", "pa_bm_block_tables", "pa_bm_block_tables_update",
-            "pa_bm_append_tokens", "pa_bm_release_window"]
+            "pa_bm_append_tokens", "pa_bm_release_window", "pa_bm_append_chunks", "pa_bm_keep"]
 
 _declared = False
 
@@ -41,6 +41,10 @@ def _lib():
         lib.pa_bm_append_token.restype = i32
         lib.pa_bm_append_tokens.argtypes = [P, P, P, i32, P, P, ctypes.POINTER(i32)]
         lib.pa_bm_append_tokens.restype = i32
+        lib.pa_bm_append_chunks.argtypes = [P, P, P, i32, P, i32, P, P, ctypes.POINTER(i32)]
+        lib.pa_bm_append_chunks.restype = i32
+        lib.pa_bm_keep.argtypes = [P, P, P, i32]
+        lib.pa_bm_keep.restype = i32
         lib.pa_bm_release_window.argtypes = [P, P, i32, i32]
         lib.pa_bm_release_window.restype = i32
         lib.pa_bm_fork.argtypes = [P, i64, i64]
@@ -135,6 +139,35 @@ class BlockManager:
                                            slots.ctypes.data, pairs.ctypes.data, ctypes.byref(k))
         _ok(rc, "pa_bm_append_tokens")
         return slots, pairs[:k.value].copy()
+
+    def append_chunks(self, seq_ids, token_lists, offer: bool = True):
+        """A run of new tokens for each listed sequence in one call (offer=False: drafts, kept out
+        of the prefix cache until `keep`). Returns (slots int64, one run after the other,
+        copy-on-write pairs int32 [k, 2] to apply before the append)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        n = len(ids)
+        if ids.ndim != 1 or len(token_lists) != n:
+            raise BlockManagerError(ERR_INVALID, "pa_bm_append_chunks")
+        counts = np.asarray([len(t) for t in token_lists], dtype=np.int32)
+        toks = np.ascontiguousarray(
+            np.concatenate([np.asarray(t, dtype=np.int32) for t in token_lists])
+            if n else np.zeros(0), dtype=np.int32)
+        slots = np.empty(len(toks), dtype=np.int64)
+        pairs = np.empty((max(n, 1), 2), dtype=np.int32)
+        k = ctypes.c_int32(0)
+        rc = self._lib.pa_bm_append_chunks(self._h, ids.ctypes.data, counts.ctypes.data, n,
+                                           toks.ctypes.data, int(offer), slots.ctypes.data,
+                                           pairs.ctypes.data, ctypes.byref(k))
+        _ok(rc, "pa_bm_append_chunks")
+        return slots, pairs[:k.value].copy()
+
+    def keep(self, seq_ids, lengths):
+        """Keep the first lengths[i] tokens of each listed sequence, drop the others."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        lens = np.ascontiguousarray(lengths, dtype=np.int32)
+        if ids.ndim != 1 or lens.shape != ids.shape:
+            raise BlockManagerError(ERR_INVALID, "pa_bm_keep")
+        _ok(self._lib.pa_bm_keep(self._h, ids.ctypes.data, lens.ctypes.data, len(ids)), "pa_bm_keep")
 
     def fork(self, parent_id: int, child_id: int):
         _ok(self._lib.pa_bm_fork(self._h, parent_id, child_id), "pa_bm_fork")

@@ -396,6 +396,134 @@ int32_t pa_bm_append_tokens(pa_block_manager* bm, const int64_t* seq_ids, const 
   return PA_BM_OK;
 }
 
+int32_t pa_bm_append_chunks(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* counts,
+                            int32_t n, const int32_t* tokens, int32_t offer, int64_t* slots,
+                            int32_t* cow_pairs, int32_t* num_pairs) {
+  if (!bm || n < 0 || !num_pairs || (n > 0 && (!seq_ids || !counts || !cow_pairs)))
+    return PA_BM_ERR_INVALID;
+  try {
+    const int32_t bs = bm->bs;
+    std::vector<Seq*> rows(static_cast<size_t>(n));
+    const uint64_t mark = ++bm->batches;
+    int64_t total = 0, need = 0;
+    // blocks: one where a shared partial last block is copied (as in
+    // blocks_for_appends), and the new ones
+    std::unordered_map<int64_t, int32_t> dropped;
+    for (int32_t i = 0; i < n; ++i) {
+      auto it = bm->seqs.find(seq_ids[i]);
+      if (it == bm->seqs.end() || it->second.batch == mark || counts[i] < 0)
+        return PA_BM_ERR_INVALID;
+      Seq& s = it->second;
+      s.batch = mark;
+      rows[static_cast<size_t>(i)] = &s;
+      const int64_t end = static_cast<int64_t>(s.length) + counts[i];
+      if (end > INT32_MAX - bs) return PA_BM_ERR_INVALID;
+      total += counts[i];
+      if (counts[i] == 0) continue;
+      if (s.length % bs != 0) {
+        const int64_t last = s.blocks.back();
+        if (bm->refcount[last] > 1) {
+          int32_t& d = dropped[last];
+          if (bm->refcount[last] - d > 1) {
+            ++need;
+            ++d;
+          }
+        }
+      }
+      need += (end + bs - 1) / bs - static_cast<int64_t>(s.blocks.size());
+    }
+    if (total > 0 && (!tokens || !slots)) return PA_BM_ERR_INVALID;
+    if (!bm->can_reclaim(need)) return PA_BM_ERR_NO_BLOCKS;
+    for (int32_t i = 0; i < n; ++i) {  // host memory first: nothing below may throw
+      Seq& s = *rows[static_cast<size_t>(i)];
+      s.tokens.reserve(s.tokens.size() + static_cast<size_t>(counts[i]));
+      s.blocks.reserve(s.blocks.size() + static_cast<size_t>(counts[i] / bs) + 2);
+    }
+    int32_t pairs = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      Seq& s = *rows[static_cast<size_t>(i)];
+      if (counts[i] == 0) continue;
+      int32_t src = -1, dst = -1;
+      if (bm->take_block(s, &src, &dst) != PA_BM_OK)
+        return PA_BM_ERR_NO_BLOCKS;  // not reached: the blocks were counted above
+      if (src >= 0) {
+        cow_pairs[2 * pairs] = src;
+        cow_pairs[2 * pairs + 1] = dst;
+        ++pairs;
+      }
+      while (static_cast<int64_t>(s.blocks.size()) * bs < static_cast<int64_t>(s.length) + counts[i]) {
+        const int64_t b = bm->alloc();
+        if (b < 0) return PA_BM_ERR_NO_BLOCKS;  // not reached
+        s.blocks.push_back(b);
+        bm->changed(s);
+      }
+    }
+    int64_t at = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      Seq& s = *rows[static_cast<size_t>(i)];
+      for (int32_t k = 0; k < counts[i]; ++k, ++at) {
+        if (offer) {
+          bm->commit_token(s, tokens[at], &slots[at]);
+        } else {
+          slots[at] = s.blocks[s.length / bs] * bs + s.length % bs;
+          s.tokens.push_back(tokens[at]);
+          ++s.length;
+        }
+      }
+    }
+    *num_pairs = pairs;
+    return PA_BM_OK;
+  } catch (...) {
+    return PA_BM_ERR_CAPACITY;
+  }
+}
+
+int32_t pa_bm_keep(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* lengths, int32_t n) {
+  if (!bm || n < 0 || (n > 0 && (!seq_ids || !lengths))) return PA_BM_ERR_INVALID;
+  try {
+    const int32_t bs = bm->bs;
+    std::vector<Seq*> rows(static_cast<size_t>(n));
+    const uint64_t mark = ++bm->batches;
+    for (int32_t i = 0; i < n; ++i) {
+      auto it = bm->seqs.find(seq_ids[i]);
+      if (it == bm->seqs.end() || it->second.batch == mark) return PA_BM_ERR_INVALID;
+      Seq& s = it->second;
+      s.batch = mark;
+      if (lengths[i] < 0 || lengths[i] > s.length ||
+          lengths[i] < static_cast<int64_t>(s.released) * bs)
+        return PA_BM_ERR_INVALID;
+      rows[static_cast<size_t>(i)] = &s;
+    }
+    for (int32_t i = 0; i < n; ++i) {
+      Seq& s = *rows[static_cast<size_t>(i)];
+      const int32_t len = lengths[i];
+      if (len < s.length) {
+        // the cached path goes back to the full blocks that stay
+        while (s.tail_blocks > len / bs) {
+          if (s.tail) s.tail = s.tail->parent == &bm->root ? nullptr : s.tail->parent;
+          --s.tail_blocks;
+        }
+        const size_t blocks = static_cast<size_t>((len + bs - 1) / bs);
+        if (blocks < s.blocks.size()) {
+          for (size_t k = blocks; k < s.blocks.size(); ++k) bm->unref(s.blocks[k]);
+          s.blocks.resize(blocks);
+          bm->changed(s);
+        }
+        s.tokens.resize(static_cast<size_t>(len));
+        s.length = len;
+      }
+      while ((s.tail_blocks + 1) * static_cast<int64_t>(bs) <= s.length && s.tail_blocks >= s.released) {
+        const int32_t before = s.tail_blocks;
+        bm->cache_full_block(s, before);
+        if (s.tail_blocks == before) break;  // cut by an eviction, or the cache is off
+      }
+    }
+    return PA_BM_OK;
+  } catch (...) {
+    return PA_BM_ERR_CAPACITY;
+  }
+}
+
 int32_t pa_bm_fork(pa_block_manager* bm, int64_t parent_id, int64_t child_id) {
   if (!bm || bm->seqs.count(child_id)) return PA_BM_ERR_INVALID;
   auto it = bm->seqs.find(parent_id);

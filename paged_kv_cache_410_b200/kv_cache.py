@@ -28,6 +28,19 @@ Prompts: ``add_sequence`` places a prompt, reusing cached prefix blocks, and
 returns the slots of the tokens whose K/V the caller still has to store
 (``store_prompt``).
 
+Chunks: ``begin_chunk`` / ``attend_chunk`` bring several new tokens per sequence
+at once -- a prompt in pieces, a mixed batch, or the drafts of a speculative
+step:
+
+    plan = cache.begin_chunk(seq_ids, [[last, d1, d2], ...], drafts=True)
+    for layer in range(num_layers):
+        out = cache.attend_chunk(plan, layer, q, k, v)   # [tokens, Hq, D]
+    accepted, tokens = cache.verify(plan, target_probs, draft_probs, u, u_sample)
+    cache.settle(plan, accepted)                         # refused drafts leave the cache
+
+``read`` returns a sequence's cached K/V as contiguous rows, and ``calibrate``
+finds an E4M3 layer's scales from K/V before the cache is first written.
+
 Several GPUs (tensor parallelism over KV heads): every rank builds a cache
 for its own heads and drives its own block manager with the same calls, so
 all ranks place every token in the same slots and no exchange is needed.
@@ -62,6 +75,24 @@ class StepPlan:
     max_context: int
     copy_pairs: np.ndarray       # int32 [k, 2] copied (every layer) before the step
     shared_prefix_blocks: int    # leading blocks every sequence's table shares
+
+
+@dataclass
+class ChunkPlan:
+    """Device-side inputs of one call that brings several new tokens per
+    sequence (shared by all layers)."""
+    seq_ids: np.ndarray
+    counts: np.ndarray           # int32 [n]: new tokens of each sequence
+    lengths: np.ndarray          # int32 [n]: tokens of each sequence with them
+    slot_mapping: torch.Tensor   # int64 [tokens]
+    cu_chunk: torch.Tensor       # int32 [n + 1]: first row of each sequence
+    block_tables: torch.Tensor   # int32 [n, max_blocks_per_seq]
+    context_lens: torch.Tensor   # int32 [n]
+    max_chunk: int
+    max_context: int
+    copy_pairs: np.ndarray       # int32 [k, 2] copied (every layer) before the call
+    drafts: torch.Tensor | None  # int32: each sequence's tokens behind its first
+    cu_drafts: torch.Tensor | None  # int32 [n + 1]
 
 
 class PagedKVCache:
@@ -126,6 +157,7 @@ class PagedKVCache:
         self._d_lens = torch.zeros(max_batch, dtype=torch.int32, device=self.device)
         self._uploaded = None      # event after the last upload (the staging is reused)
         self._workspace = None
+        self._amax = [None] * num_layers   # running max-abs of calibrated layers (K, V)
 
     # ---- sequences -------------------------------------------------------------
     def add_sequence(self, seq_id: int, token_ids):
@@ -233,6 +265,144 @@ class PagedKVCache:
                                plan.block_tables, plan.context_lens, scale, out, cache,
                                plan.max_context, workspace=ws, stream=self.stream)
         return out
+
+    # ---- several new tokens per sequence -----------------------------------------
+    def begin_chunk(self, seq_ids, token_lists, drafts: bool = False) -> ChunkPlan:
+        """Reserve a run of new tokens (token_lists[i], may be empty) for each
+        listed sequence, copy the blocks forked sequences diverge on (every
+        layer) and upload slots, row starts, tables and lengths. With `drafts`
+        each run is the sequence's last sampled token and its drafts: they stay
+        out of the prefix cache until `settle` keeps some of them. A bad id, or
+        a pool that cannot supply the call, raises with nothing reserved."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        counts = np.asarray([len(t) for t in token_lists], dtype=np.int32)
+        if len(counts) != len(ids):
+            raise ValueError("one list of tokens per sequence")
+        if drafts and (counts < 1).any():
+            raise ValueError("a speculative step brings every sequence's last token at least")
+        for s, c in zip(ids, counts):
+            if -(-(self.bm.length(int(s)) + int(c)) // self.block_size) > self.max_blocks:
+                raise ValueError(f"sequence {s} would outgrow {self.max_blocks} blocks")
+        slots, pairs = self.bm.append_chunks(ids, token_lists, offer=not drafts)
+        if len(pairs):
+            B.pa_copy_blocks_layers(pairs, self.k, self.v, self.layers[0], self.stream)
+        tables, lens = self.bm.block_tables(ids, self.max_blocks)
+        if self.window:
+            # blocks that hold only tokens before the first new token's window
+            for s, n, c in zip(ids, lens, counts):
+                self.bm.release_before(int(s), max(0, int(n) - int(c) - self.window + 1))
+        if self.lockstep_group is not None:
+            self._check_lockstep(slots, pairs, lens)
+        cu = np.zeros(len(ids) + 1, dtype=np.int32)
+        np.cumsum(counts, out=cu[1:])
+        cu_drafts = (cu - np.arange(len(ids) + 1)).astype(np.int32) if drafts else None
+        later = None
+        if drafts:
+            later = np.concatenate([np.asarray(t[1:], dtype=np.int32) for t in token_lists]
+                                   or [np.zeros(0, np.int32)]).astype(np.int32)
+        with self._on_stream():
+            up = lambda a: None if a is None else torch.from_numpy(a).to(self.device)  # noqa: E731
+            return ChunkPlan(seq_ids=ids, counts=counts, lengths=lens, slot_mapping=up(slots),
+                             cu_chunk=up(cu), block_tables=up(tables), context_lens=up(lens),
+                             max_chunk=int(counts.max(initial=0)),
+                             max_context=int(lens.max(initial=0)), copy_pairs=pairs,
+                             drafts=up(later), cu_drafts=up(cu_drafts))
+
+    def attend_chunk(self, plan: ChunkPlan, layer: int, q, k, v, scale: float | None = None,
+                     out=None):
+        """Store this layer's new K/V (k, v [tokens, Hkv, D]) at the plan's
+        slots and return the attention [tokens, Hq, D] of queries q over each
+        sequence's cache up to the row's own token (the last `window` of them
+        with a window): pa_append_kv and pa_attend_chunk."""
+        if out is None:
+            out = torch.empty_like(q)
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.head_dim)
+        cache = self.layers[layer]
+        B.pa_append_kv(k, v, plan.slot_mapping, self.k[layer], self.v[layer], cache, self.stream)
+        need = B.pa_attend_chunk_workspace_size(q.shape[0], len(plan.seq_ids), q.shape[1],
+                                                plan.max_chunk, plan.max_context, cache,
+                                                window=self.window)
+        if need and (self._workspace is None or self._workspace.numel() < need):
+            with self._on_stream():
+                self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        B.pa_attend_chunk(q, self.k[layer], self.v[layer], plan.cu_chunk, plan.block_tables,
+                          plan.context_lens, scale, out, cache, plan.max_chunk, plan.max_context,
+                          window=self.window, workspace=self._workspace if need else None,
+                          stream=self.stream)
+        return out
+
+    def verify(self, plan: ChunkPlan, target_probs, draft_probs, accept_uniforms,
+               sample_uniforms):
+        """Which of a speculative plan's drafts the target keeps (pa_verify_draft):
+        target_probs [tokens, vocab] are the rows behind every token of the plan,
+        draft_probs [drafts, vocab] (or None) those the drafts were drawn from.
+        Returns device tensors accepted [n] and tokens [n, max_chunk] (accepted
+        drafts, the drawn token, then -1)."""
+        if plan.drafts is None:
+            raise ValueError("the plan has no drafts (begin_chunk(drafts=True))")
+        n = len(plan.seq_ids)
+        with self._on_stream():
+            accepted = torch.empty(n, dtype=torch.int32, device=self.device)
+            tokens = torch.empty((n, max(plan.max_chunk, 1)), dtype=torch.int32,
+                                 device=self.device)
+        B.pa_verify_draft(plan.drafts, plan.cu_drafts, target_probs, draft_probs,
+                          accept_uniforms, sample_uniforms, accepted, tokens, self.stream)
+        return accepted, tokens
+
+    def settle(self, plan: ChunkPlan, accepted):
+        """Keep a speculative plan's last sampled tokens and their accepted drafts
+        (accepted: [n] counts, on any device; read on the host) and drop the
+        refused ones from the sequences."""
+        if plan.drafts is None:
+            raise ValueError("the plan has no drafts (begin_chunk(drafts=True))")
+        if isinstance(accepted, torch.Tensor):
+            with self._on_stream():
+                accepted = accepted.cpu().numpy()
+        a = np.asarray(accepted, dtype=np.int64)
+        if a.shape != plan.counts.shape or (a < 0).any() or (a >= plan.counts).any():
+            raise ValueError("accepted: between 0 and the drafts of each sequence")
+        self.bm.keep(plan.seq_ids, plan.lengths - plan.counts + 1 + a)
+
+    # ---- reading back, calibration -------------------------------------------------
+    def read(self, layer: int, seq_id: int, first: int = 0, count: int | None = None):
+        """The cached K and V of a sequence's tokens [first, first + count) (to its
+        end without `count`) as contiguous [count, Hkv, D] tensors in io_dtype
+        (an E4M3 cache's codes times their scales)."""
+        length = self.bm.length(seq_id)
+        count = length - first if count is None else count
+        if first < 0 or count < 0 or first + count > length:
+            raise ValueError(f"tokens [{first}, {first + count}) of {length}")
+        if count:
+            self.bm.slots(seq_id, first, count)   # (raises for blocks the window has released)
+        tables, _ = self.bm.block_tables([seq_id], self.max_blocks)
+        with self._on_stream():
+            k = torch.empty((count, self.num_kv_heads, self.head_dim), dtype=self.io_dtype,
+                            device=self.device)
+            v = torch.empty_like(k)
+            up = lambda a: torch.tensor(a, dtype=torch.int32, device=self.device)  # noqa: E731
+            B.pa_gather_kv(self.k[layer], self.v[layer], torch.from_numpy(tables).to(self.device),
+                           up([first]), up([0, count]), k, v, self.layers[layer], self.stream)
+        return k, v
+
+    def calibrate(self, layer: int, k, v, slot_mapping=None):
+        """Scales of an E4M3 layer from K/V it is to hold (k, v [T, Hkv, D]; tokens
+        with a negative slot do not count): max |x| / 448 per (head, channel) over
+        this and all earlier calls on the layer, in place of the scales the cache
+        was made with. Call it before the layer is first written: tokens stored
+        under other scales keep their codes."""
+        if not self.e4m3:
+            raise ValueError("only an E4M3 cache has scales")
+        with self._on_stream():
+            if self._amax[layer] is None:
+                new = lambda: torch.zeros((self.num_kv_heads, self.head_dim),  # noqa: E731
+                                          dtype=torch.float32, device=self.device)
+                self._amax[layer] = (new(), new())
+                c = self.layers[layer]
+                c.k_scale, c.v_scale, c.k_inv_scale, c.v_inv_scale = new(), new(), new(), new()
+            c = self.layers[layer]
+            B.pa_calibrate_kv(k, v, slot_mapping, *self._amax[layer], c.k_scale, c.v_scale,
+                              c.k_inv_scale, c.v_inv_scale, self.stream)
 
     def _check_lockstep(self, slots, pairs, lens):
         import torch.distributed as dist
