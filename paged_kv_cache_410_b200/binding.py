@@ -158,9 +158,21 @@ def _dev(t, name: str, dtypes=None, shape=None) -> int | None:
         raise ValueError(f"{name}: expected a contiguous CUDA tensor")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-    if shape is not None and t.shape != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
+
+
+def _on_current(*tensors):
+    """The launch goes to the current device: tensors of another are refused
+    (a kernel could not reach them)."""
+    at = tensors[0].get_device()
+    if at >= 0 and at != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{at}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for t in tensors[1:]:
+        if t is not None and t.get_device() != at:
+            raise ValueError("tensors on more than one device")
 
 
 def _nbytes(t) -> int:
@@ -444,6 +456,7 @@ def pa_attend_chunk(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, s
     if block_tables.dim() != 2:
         raise ValueError("block_tables: expected [batch, max_blocks_per_seq]")
     batch, hq = block_tables.shape[0], q.shape[1]
+    _on_current(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, out, workspace)
     pq = _dev(q, "q", _IO, (q.shape[0], hq, cache.head_dim))
     pt = _dev(block_tables, "block_tables", (torch.int32,))
     pl = _dev(context_lens, "context_lens", (torch.int32,), (batch,))
@@ -473,6 +486,8 @@ def pa_verify_draft(draft_tokens, cu_drafts, target_probs, draft_probs, accept_u
     n, batch, vocab = draft_tokens.numel(), accepted.numel(), target_probs.shape[1]
     if tokens.shape[1] < 1:
         raise ValueError("tokens: expected [batch, max_drafts + 1]")
+    _on_current(target_probs, draft_probs, draft_tokens, cu_drafts, accept_uniforms,
+                sample_uniforms, accepted, tokens)
     i32, f32 = (torch.int32,), (torch.float32,)
     pp = _dev(target_probs, "target_probs", _PROBS, (n + batch, vocab))
     pq = _dev(draft_probs, "draft_probs", (target_probs.dtype,), (n, vocab))
@@ -498,6 +513,7 @@ def pa_calibrate_kv(k, v, slot_mapping, k_amax, v_amax, k_scale, v_scale, k_inv_
     if k.dim() != 3:
         raise ValueError("k: expected [num_tokens, num_kv_heads, head_dim]")
     t, hkv, hd = k.shape
+    _on_current(k, v, slot_mapping, k_amax, v_amax, k_scale, v_scale, k_inv_scale, v_inv_scale)
     pk = _dev(k, "k", _IO, (t, hkv, hd))
     pv = _dev(v, "v", (k.dtype,), (t, hkv, hd))
     arrays = [_dev(a, name, (torch.float32,), (hkv, hd)) for a, name in
@@ -522,6 +538,7 @@ def pa_gather_kv(k_cache, v_cache, block_tables, first, cu_tokens, k_out, v_out,
         raise ValueError("block_tables: expected [batch, max_blocks_per_seq]")
     batch, t = block_tables.shape[0], k_out.shape[0]
     shape = (t, cache.num_kv_heads, cache.head_dim)
+    _on_current(k_cache, v_cache, block_tables, first, cu_tokens, k_out, v_out)
     i32 = (torch.int32,)
     kc, vc = cache.cache_ptrs(k_cache, v_cache)
     rc = lib.pa_gather_kv(kc, vc, ctypes.byref(d), _dev(block_tables, "block_tables", i32),

@@ -216,6 +216,21 @@ def test_binding_checks(rec):
         B.pa_gather_kv(k, k, i32(2, 4), i32(2), i32(3), kk, kk.bfloat16(), cache, stream=0)
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    class Fake:
+        def __init__(self, at):
+            self.at = at
+
+        def get_device(self):
+            return self.at
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    B._on_current(Fake(0), None, Fake(0))
+    for bad in ((Fake(1), Fake(1)), (Fake(0), Fake(1))):
+        with pytest.raises(ValueError):
+            B._on_current(*bad)
+
+
 # ---- block manager -------------------------------------------------------------
 def test_chunks_equal_single_appends():
     a, b = BlockManager(64, 4, True), BlockManager(64, 4, True)
