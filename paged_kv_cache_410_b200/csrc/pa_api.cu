@@ -808,7 +808,8 @@ ChunkPlan make_chunk_plan(int64_t num_tokens, int64_t batch, int64_t num_q_heads
   pl.tile_tokens = pa::kUmmaRows / pl.head_rows;
   pl.tiles_per_cta = max_chunk > pl.tile_tokens ? 2 : 1;
   const int64_t t = static_cast<int64_t>(pl.tiles_per_cta) * pl.tile_tokens;
-  const int64_t tiles = num_tokens / t + batch;  // chunk_tile's bound
+  // chunk_tile's bound (one per sequence where each is one tile)
+  const int64_t tiles = pl.tiles_per_cta == 1 ? batch : num_tokens / t + batch;
   pl.num_tiles = static_cast<int>(tiles);
   // tokens a CTA tile can attend, from its first (rounded) token
   int64_t span = std::max<int64_t>(max_context, 1);
@@ -1072,6 +1073,12 @@ pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, in
   p.head_blocks = pl.head_blocks;
   p.tile_tokens = pl.tile_tokens;
   p.num_tiles = pl.num_tiles;
+  p.one_tile = pl.tiles_per_cta == 1;
+  // more CTAs than the GPU holds at once: their order decides how they end
+  p.longest_first = p.one_tile && batch > 1 && batch <= pa::kChunkOrderMax &&
+                    static_cast<int64_t>(batch) * p.num_kv_heads * p.head_blocks *
+                            p.num_partitions >
+                        2 * kNumSMs;
   p.num_partitions = pl.num_partitions;
   p.partition_tokens = pl.partition_tokens;
   p.max_blocks_per_seq = max_blocks_per_seq;

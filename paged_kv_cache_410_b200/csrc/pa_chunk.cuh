@@ -53,6 +53,8 @@ struct ChunkParams {
   int head_blocks;            // ceil(group / head_rows)
   int tile_tokens;            // new tokens in one row tile: 128 / head_rows
   int num_tiles;              // grid bound: CTA tiles over the batch
+  int one_tile;               // every chunk fits one tile of a one-tile CTA
+  int longest_first;          // (one_tile) visit the longest contexts first
   int num_partitions;
   int partition_tokens;       // a multiple of the kernel's BN
   int max_blocks_per_seq;
@@ -79,10 +81,11 @@ struct ChunkTile {
 // Tiles are laid over the batch without reading lengths on the host: sequence
 // b owns tile indices from f(b) = cu[b] / t + b (t tokens per tile), which
 // leaves it at least ceil(n_b / t) of them; surplus tiles have no rows. One
-// warp finds b, the last sequence with f(b) <= x, 32 probes at a time.
+// warp finds b, the last sequence with f(b) <= x, 32 probes at a time. When
+// every chunk fits one tile, x is the sequence itself.
 __device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int t) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = p.batch;
+  int lo = p.one_tile ? x : 0, hi = p.one_tile ? x + 1 : p.batch;
   while (hi - lo > 1) {
     const int stride = (hi - lo + 31) >> 5;
     const int at = lo + lane * stride;
@@ -105,7 +108,7 @@ __device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int
     return c;
   }
   const int n = end - start;
-  const int64_t first = static_cast<int64_t>(x - (start / t + lo)) * t;
+  const int64_t first = p.one_tile ? 0 : static_cast<int64_t>(x - (start / t + lo)) * t;
   if (first < 0 || first >= n) return c;
   c.b = lo;
   c.i0 = static_cast<int>(first);
@@ -122,6 +125,35 @@ __device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int
   c.lo = p.window > 0 ? max(0, c.pos0 - p.window + 1) : 0;
   c.base = c.lo / kChunkStep * kChunkStep;
   return c;
+}
+
+// The sequence with the x-th longest context (ties: the lower index first), by
+// one warp: the key's bits are fixed from the top by counting the keys that
+// are not below the candidate.
+constexpr int kChunkOrderMax = 256;
+__device__ __forceinline__ int chunk_longest(const ChunkParams& p, int x) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[kChunkOrderMax / 32];
+#pragma unroll
+  for (int k = 0; k < kChunkOrderMax / 32; ++k) {
+    const int b = lane + 32 * k;
+    key[k] = 0;
+    if (b < p.batch) {
+      int L = max(0, min(__ldg(p.context_lens + b), (1 << 22) - 1));
+      if (p.window > 0) L = min(L, p.window + p.max_chunk);
+      key[k] = (static_cast<uint32_t>(L + 1) << 8) | static_cast<uint32_t>(255 - b);
+    }
+  }
+  uint32_t found = 0;
+  for (int bit = 30; bit >= 0; --bit) {
+    const uint32_t cand = found | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kChunkOrderMax / 32; ++k)
+      if (32 * k < p.batch) n += __popc(__ballot_sync(0xffffffffu, key[k] >= cand));
+    if (n > x) found = cand;
+  }
+  return 255 - static_cast<int>(found & 255u);
 }
 
 // MODE: how K / V reach shared memory.
@@ -282,8 +314,7 @@ __device__ __forceinline__ void set_fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
-// Grid: tiles x KV heads x head blocks x partitions, partition fastest, the
-// batch's last tiles first (in a causal chunk they see the most tokens).
+// Grid: tiles x KV heads x head blocks x partitions, partition fastest.
 template <typename TQ, int D, int NT, int MODE>
 __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
                                   ChunkCfg<D, NT, MODE>::kCtas)
@@ -338,7 +369,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   const int hb = u % p.head_blocks;
   u /= p.head_blocks;
   const int hk = u % p.num_kv_heads;
-  const int x = p.num_tiles - 1 - u / p.num_kv_heads;
+  // the batch's last tiles first (in a causal chunk they see the most tokens);
+  // where every sequence is one tile, the longest contexts first (drafts of 64
+  // requests with 512 to 4096 tokens: 138 -> 118 us)
+  int x = p.num_tiles - 1 - u / p.num_kv_heads;
+  if (NT == 1 && p.longest_first) {
+    if (warp == 0) {
+      const int b = chunk_longest(p, u / p.num_kv_heads);
+      if (lane == 0) asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(tmem_slot), "r"(b) : "memory");
+    }
+    __syncthreads();
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(x) : "r"(tmem_slot));
+    __syncthreads();  // (the slot receives the TMEM address next)
+  }
   const ChunkTile ct = chunk_tile(p, x, NT * p.tile_tokens);
   if (ct.b < 0) return;
   const int h0 = hk * p.group + hb * p.head_rows;                 // first query head
