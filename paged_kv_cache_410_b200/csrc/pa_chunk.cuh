@@ -8,21 +8,46 @@
 //
 // For one KV head the rows (token, query head of the group) of a run of new
 // tokens against the cached tokens are a dense problem, so a CTA takes NT
-// tiles of up to 128 such rows and walks the tokens in steps of BN:
-//   S (128 x BN, f32, TMEM)     = Q (128 x D, smem) . K_step^T (BN x D, smem)
-//   P (128 x BN, 16-bit, TMEM)  = 2^(S - m), over S's own columns
-//   O (128 x D, f32, TMEM)     += P (TMEM) . V_step (BN x D, smem)
-// with the running maximum m and sum l of a row in the registers of the one
-// thread that owns the row. K and V steps come through one ring of NBUF
-// buffers (K0 V0 K1 V1 ...), filled by one TMA warp (16-bit caches with
-// blocks of 8 tokens or more: whole 1024-byte swizzle atoms per box), or by
-// four loader warps with cp.async (smaller blocks; E4M3 caches, which they
-// widen to f16: exact).
+// tiles of up to 128 such rows and walks the tokens in steps of 64:
+//   S (128 x 64, f32, TMEM, two buffers) = Q (128 x D, smem) . K_step^T
+//   P (128 x 64, 16-bit, TMEM)           = 2^(S - m), over S's own columns
+//   O (128 x D, f32, TMEM)              += P (TMEM) . V_step (64 x D, smem)
+// with the running maximum m and sum l of a row, in 32 bits, in the registers
+// of the one thread that owns the row. P is rounded to the operands' 16 bits
+// (2^-8 or 2^-11 of each weight: what the MMA takes); l sums the weights
+// before that rounding. m moves only when a score passes it by 2^8, so that O
+// is rarely rescaled.
+//
+// K and V steps come through one ring of buffers (K0 V0 K1 V1 ...), filled by
+// two TMA warps (16-bit caches with blocks of 8 tokens or more: whole
+// 1024-byte swizzle atoms per box), or by four loader warps with cp.async
+// (smaller blocks; E4M3 caches, which they widen to f16: exact; the K scale is
+// folded into q, rounded once to f16, and the V scale into the result).
 //
 // What each row may not see is decided by selecting on S, so K of masked
 // tokens never matters; V rows outside the CTA's token range (behind the
 // last row's position, before the first row's window: recycled memory) are
 // zeroed in shared memory, since 0 x NaN would reach the sum.
+//
+// What bounds it, measured on one B200 (1.9 GHz, device time):
+//  - drafts (64 requests, 2 to 8 new tokens, 512 to 4096 cached ones, 64 / 8
+//    heads of 128, bf16): 118 to 141 us on different GPUs for 636 MB, 0.69 to
+//    0.82 of the copy bandwidth.
+//    One-tile CTAs, two per SM; without the loads the launch takes 103 us,
+//    without the softmax 131: the loads and the tail are what is left.
+//  - prompts (2048 tokens over 16384, 64 / 8 heads, bf16): 910 us (1030
+//    under the power cap of a long run), 1.0 to 1.1 PFLOP/s, 0.6 to 0.66 of the
+//    cuBLAS burst. A step of 64 tokens and 256 rows takes about
+//    1850 clocks. Its MMAs alone take 1300 (a tcgen05.mma of N = 64 runs in 33
+//    (A in TMEM) to 49 clocks, but one warp needs 60 to issue it), its
+//    exponentials 1024; the rest is the chain S -> P -> P.V -> S of a tile
+//    (about 110 clocks a wait, 60 a commit). Steps that were tried and lost: N = 128
+//    with one S buffer per tile (the MMAs alone 1030 a step, but the two tiles
+//    fall into step and wait together: 1277 us in all), two warps per row
+//    (1526 us), one MMA warp per tile instead of two (1003 us), a quarter of the
+//    exponentials as polynomials on the FMA pipe (976 against 937 us).
+//  - E4M3 (a mixed batch of 32, 32 / 8 heads): 240 us; the loader warps'
+//    widening, 128 threads for 16 KB of codes a step, is the pace.
 #pragma once
 
 #include "pa_prefix_umma.cuh"
