@@ -373,11 +373,12 @@ size_t pa_attend_chunk_workspace_size(int64_t num_tokens, int32_t batch, int32_t
  * this is pa_decode; a mixed batch (some sequences decoding one token, some
  * running a prompt chunk, some bringing none) is one call.
  *   q, out        [num_tokens][num_q_heads][head_dim] in q_dtype (for a
- *                 16-bit cache, its dtype). Rows outside cu_chunk[0] ..
+ *                 16-bit cache, its dtype); out may be q. Rows outside cu_chunk[0] ..
  *                 cu_chunk[batch] (padding) are left as they were.
  *   cu_chunk      [batch + 1] int32, not decreasing, within [0, num_tokens].
  *   max_chunk     host-side upper bound of the n_b (sizes the launch).
- *   block_tables, context_lens, max_context, scale: as for pa_decode;
+ *   block_tables, context_lens, max_context (at most 2^30), scale: as for
+ *                 pa_decode; at most 2000 query heads;
  *                 context_lens[b] includes the n_b new tokens. Table entries
  *                 of blocks behind the sequence's last token, or holding only
  *                 tokens before the first row's window, are not read.
@@ -453,7 +454,8 @@ pa_status pa_verify_draft(const int32_t* draft_tokens, int64_t num_drafts, int32
  *                 pa_cache_desc. Tokens appended under other scales keep their
  *                 codes: calibrate before the cache is first written.
  * Infinities and NaN do not count. num_tokens == 0 leaves amax and writes the
- * scales. Every pointer is 16-byte aligned. */
+ * scales. Every pointer is 16-byte aligned. Calls on the same arrays must not
+ * overlap (other streams): a call reads amax, then writes it. */
 pa_status pa_calibrate_kv(const void* k, const void* v, int32_t in_dtype, int64_t num_tokens,
                           int32_t num_kv_heads, int32_t head_dim, const int64_t* slot_mapping,
                           float* k_amax, float* v_amax, float* k_scale, float* v_scale,

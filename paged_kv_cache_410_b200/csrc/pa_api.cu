@@ -869,7 +869,6 @@ pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const 
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   if (p.num_partitions == 1) return PA_OK;
   const int64_t rows = static_cast<int64_t>(NT) * p.tile_tokens * p.num_q_heads;
-  if ((rows + 7) / 8 > 65535) return PA_ERR_UNSUPPORTED;
   return launch_dependent(pa::pa_chunk_merge_kernel<TQ, D>,
                           dim3(p.num_tiles, static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,
                           st, p, NT * p.tile_tokens) == cudaSuccess
@@ -1040,7 +1039,11 @@ pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, in
   if (batch < 0) return PA_ERR_INVALID_ARG;
   if (nothing) return PA_OK;
   if (!cu_chunk) return PA_ERR_INVALID_ARG;
-  if (num_tokens > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+  // (positions plus a step or a partition stay below 2^31)
+  if (num_tokens > 0x7fffffffLL || max_context > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  // a merge launch covers a CTA's rows with a 16-bit grid dimension
+  if (num_q_heads > 2000) return PA_ERR_UNSUPPORTED;
+  if (window >= max_context) window = 0;  // no row sees more than its context
   max_chunk = static_cast<int32_t>(std::min<int64_t>(max_chunk, num_tokens));
   const ChunkPlan pl = make_chunk_plan(num_tokens, batch, num_q_heads, max_chunk, max_context,
                                        window, partition_tokens, cache);

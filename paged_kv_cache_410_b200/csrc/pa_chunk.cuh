@@ -165,7 +165,7 @@ __device__ __forceinline__ int chunk_longest(const ChunkParams& p, int x) {
     key[k] = 0;
     if (b < p.batch) {
       int L = max(0, min(__ldg(p.context_lens + b), (1 << 22) - 1));
-      if (p.window > 0) L = min(L, p.window + p.max_chunk);
+      if (p.window > 0) L = min(L, p.window);
       key[k] = (static_cast<uint32_t>(L + 1) << 8) | static_cast<uint32_t>(255 - b);
     }
   }
@@ -178,7 +178,7 @@ __device__ __forceinline__ int chunk_longest(const ChunkParams& p, int x) {
       if (32 * k < p.batch) n += __popc(__ballot_sync(0xffffffffu, key[k] >= cand));
     if (n > x) found = cand;
   }
-  return 255 - static_cast<int>(found & 255u);
+  return min(255 - static_cast<int>(found & 255u), p.batch - 1);
 }
 
 // MODE: how K / V reach shared memory.

@@ -272,8 +272,10 @@ class PagedKVCache:
         listed sequence, copy the blocks forked sequences diverge on (every
         layer) and upload slots, row starts, tables and lengths. With `drafts`
         each run is the sequence's last sampled token and its drafts: they stay
-        out of the prefix cache until `settle` keeps some of them. A bad id, or
-        a pool that cannot supply the call, raises with nothing reserved."""
+        out of the prefix cache until `settle` keeps some of them (before the
+        sequences' next call). Without, their full blocks are offered to later
+        prompts at once: attend every layer before the next add_sequence. A bad
+        id, or a pool that cannot supply the call, raises with nothing reserved."""
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
         counts = np.asarray([len(t) for t in token_lists], dtype=np.int32)
         if len(counts) != len(ids):

@@ -50,7 +50,8 @@ def attend(lib, d=None, **kw):
     (dict(out=ctypes.c_void_p(24)), INVALID), (dict(mb=0), INVALID), (dict(ctx=-1), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(part=64), INVALID), (dict(part=200), INVALID), (dict(part=1 << 21), INVALID),
-    (dict(batch=70000), UNSUPPORTED),
+    (dict(batch=70000), UNSUPPORTED), (dict(ctx=(1 << 30) + 1), UNSUPPORTED),
+    (dict(hq=2002), UNSUPPORTED),
     (dict(ctx=4096, part=128), WORKSPACE),                                   # none given
     (dict(ctx=4096, part=128, ws=P, wsb=100), WORKSPACE),                    # too small
     (dict(ctx=4096, part=128, ws=ctypes.c_void_p((1 << 20) + 16), wsb=1 << 30), WORKSPACE),

@@ -135,6 +135,29 @@ def test_many_sequences():
     check(c, got)
 
 
+@pytest.mark.parametrize("window", [0, 50, 2 ** 31 - 1])
+def test_longest_first(window):
+    """More one-tile CTAs than the GPU holds: visited by context length, equal ones by index."""
+    chunks = [(i * 3) % 5 for i in range(45)]
+    ctxs = [c + [0, 7, 7, 100, 64, 3][i % 6] for i, c in enumerate(chunks)]
+    c = chunk_case(45, 8, 8, 64, 16, F16, chunks, ctxs, pad=2)
+    got = call(on_gpu(c), window=window)
+    assert B.pa_get_device_error() == 0
+    check(c, got, min(window, 1000))
+    # the same with chunks longer than a row tile (two-tile CTAs)
+    c = chunk_case(3, 2, 1, 64, 16, BF16, [70, 1, 140], [70, 90, 150])
+    check(c, call(on_gpu(c), window=window), min(window, 1000))
+
+
+def test_in_place():
+    """The result may overwrite the queries."""
+    c = chunk_case(2, 8, 2, 128, 16, BF16, [50, 3], [120, 400])
+    g = on_gpu(c)
+    want = call(g)
+    q = g["q"].clone()
+    assert torch.equal(call(dict(g, q=q), out=q), want)
+
+
 @pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0, 1e-6])
 def test_scales(scale):
     c = chunk_case(2, 4, 2, 64, 16, F16, [9, 2], [50, 150])
