@@ -46,8 +46,9 @@
 //    fall into step and wait together: 1277 us in all), two warps per row
 //    (1526 us), one MMA warp per tile instead of two (1003 us), a quarter of the
 //    exponentials as polynomials on the FMA pipe (976 against 937 us).
-//  - E4M3 (a mixed batch of 32, 32 / 8 heads): 240 us; the loader warps'
-//    widening, 128 threads for 16 KB of codes a step, is the pace.
+//  - E4M3 (a mixed batch of 32, 32 / 8 heads): 240 us; the same batch from a f16
+//    cache 136: the loader warps' copies in flight and widening set the pace
+//    (twice the loader warps: 248).
 #pragma once
 
 #include "pa_prefix_umma.cuh"
@@ -80,6 +81,8 @@ struct ChunkParams {
   int num_tiles;              // grid bound: CTA tiles over the batch
   int one_tile;               // every chunk fits one tile of a one-tile CTA
   int longest_first;          // (one_tile) visit the longest contexts first
+  int min_new, max_new;       // the chunk lengths this launch takes (a mixed batch has two)
+  int leading, trailing;      // the first, the second launch of a mixed batch
   int num_partitions;
   int partition_tokens;       // a multiple of the kernel's BN
   int max_blocks_per_seq;
@@ -133,6 +136,7 @@ __device__ __forceinline__ ChunkTile chunk_tile(const ChunkParams& p, int x, int
     return c;
   }
   const int n = end - start;
+  if (n < p.min_new || n > p.max_new) return c;
   const int64_t first = p.one_tile ? 0 : static_cast<int64_t>(x - (start / t + lo)) * t;
   if (first < 0 || first >= n) return c;
   c.b = lo;
@@ -379,6 +383,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
+
+  // A mixed batch's second launch may start once every CTA of the first has
+  // (they share nothing), and must not end before it, since work behind the
+  // call waits for the second only: its last CTA waits for the first.
+  if (p.leading) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (p.trailing && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // one CTA looks at the whole of cu: chunks that overlap, run backwards or
   // leave [0, num_tokens) may own no tile that would notice

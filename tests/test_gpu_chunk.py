@@ -149,6 +149,23 @@ def test_longest_first(window):
     check(c, call(on_gpu(c), window=window), min(window, 1000))
 
 
+@pytest.mark.parametrize("cache", ["io", "e4m3"])
+@pytest.mark.parametrize("window", [0, 30])
+def test_mixed_batch_of_many(cache, window):
+    """Chunks longer than a row tile among many single tokens and empty chunks: two launches."""
+    chunks = [140 if i in (3, 38) else 70 if i == 17 else (i % 4 != 1) * 1 for i in range(40)]
+    ctxs = [c + (i * 13) % 90 for i, c in enumerate(chunks)]
+    c = chunk_case(40, 16, 8, 64, 16, F16, chunks, ctxs, cache, pad=2)
+    g = on_gpu(c)
+    got = call(g, window=window)
+    # work enqueued behind the call sees both launches' results
+    copy = call(g, window=window).clone()
+    assert B.pa_get_device_error() == 0
+    check(c, got, window)
+    assert torch.equal(got, copy)
+    assert torch.equal(got[-2:].cpu(), c["out"][-2:])
+
+
 def test_in_place():
     """The result may overwrite the queries."""
     c = chunk_case(2, 8, 2, 128, 16, BF16, [50, 3], [120, 400])
