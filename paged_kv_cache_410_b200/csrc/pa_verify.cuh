@@ -58,8 +58,12 @@ __device__ __forceinline__ float2 exact_difference(float a, float b) {
   return make_float2(s, __fsub_rn(__fsub_rn(a, __fsub_rn(s, t)), __fadd_rn(b, t)));
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
+// The two halves of a barrier over the cluster's CTAs; each is executed by
+// converged warps (.aligned).
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
 }
 
@@ -130,6 +134,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) pa_verify_kernel(const Veri
     if (rank == 0 && threadIdx.x == 0) flag_error(PA_DEVERR_CHUNK);
     return;
   }
+  // A CTA's shared memory may be written from the others only once it is known
+  // to have started: every CTA says so here, and waits for all before its
+  // first store (the reads of the row lie between).
+  if constexpr (CL > 1) cluster_arrive();
   const int64_t V = p.vocab;
   const T* target = reinterpret_cast<const T*>(p.target_probs) + (static_cast<int64_t>(start) + b) * V;
   const T* draft = p.draft_probs ? reinterpret_cast<const T*>(p.draft_probs) + start * V : nullptr;
@@ -181,6 +189,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) pa_verify_kernel(const Veri
       if (lane == 0) sums[attempt][g] = s;
       __syncthreads();
     } else {
+      if (attempt == 0) cluster_wait();  // (every CTA of the cluster has started)
       if (lane < CL) {
         uint32_t at;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n"
@@ -188,7 +197,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) pa_verify_kernel(const Veri
                      : "r"(smem_addr(&sums[attempt][g])), "r"(lane));
         asm volatile("st.shared::cluster.f64 [%0], %1;\n" ::"r"(at), "d"(s) : "memory");
       }
-      cluster_sync_all();
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
     }
     // the pieces' running sums: lane holds PL consecutive ones
     constexpr int PL = (kPieces + 31) / 32;

@@ -54,6 +54,26 @@ def test_verify(vocab, dtype, has_q):
     assert got[1] == want[1]
 
 
+@pytest.mark.parametrize("batch", [37, 38, 74, 75, 148, 149, 160])
+@pytest.mark.parametrize("vocab", [1, 5, 64, 1003, 2048])
+@pytest.mark.parametrize("has_q", [True, False])
+def test_verify_every_cluster_size(batch, vocab, has_q):
+    """A sequence is taken by a cluster of 8, 4, 2 or 1 CTAs, by the batch: both sides of each
+    border, for vocabularies whose warps reach the exchange at once, and without drafts."""
+    counts = [(0, 2, 1, 4, 0, 0, 3)[i % 7] for i in range(batch)]
+    for dtype in (F32, BF16):
+        drafts, cu, target, draft, ua, us = draft_case(counts, vocab, dtype, 2.0, batch + vocab)
+        ua *= 0.7
+        if not has_q:
+            draft = None
+        want = verify_draft(drafts, cu, target, draft, ua, us, 4)
+        for _ in range(2):
+            got = run_verify(drafts, cu, target, draft, ua, us, 4)
+            assert B.pa_get_device_error() == 0
+            assert got[0] == want[0]
+            assert got[1] == want[1]
+
+
 def test_verify_nothing_left_of_the_difference():
     """p <= q everywhere (rows need not be normalised): the draw is from p."""
     drafts, cu, target, draft, ua, us = draft_case([2, 2], 513, F32, 1.0, 3)
