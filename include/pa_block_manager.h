@@ -81,7 +81,8 @@ int32_t pa_bm_append_token(pa_block_manager* bm, int64_t seq_id, int32_t token, 
  * to cow_pairs ([n][2] int32 (src, dst), room for n pairs) and their count to
  * *num_pairs; apply them (pa_copy_blocks) before appending K/V. A sequence
  * that copies drops its share of the old block, so a later sequence of the
- * batch that shared it with that one alone writes in place. The batch's
+ * batch that shared it with that one alone writes in place. No block is the
+ * source of one pair and the destination of another. The batch's
  * blocks are all taken before any of its tokens joins the prefix cache, so
  * when the pool must evict cached blocks the choice can differ from n
  * separate pa_bm_append_token calls (both placements are valid). Returns

@@ -185,6 +185,23 @@ struct pa_block_manager {
     return PA_BM_OK;
   }
 
+  // A block that a batch copies from must not be handed out within the batch:
+  // its copy would then be one of those the batch makes at the same time (a
+  // source of one pair, the destination of another). Where the sequence that
+  // copied was its last one and only the cache holds it now, it takes a
+  // reference until the batch has all its blocks (so it cannot be evicted;
+  // blocks_for_appends did not count it as reclaimable, since the sequence
+  // still held it). A block that another sequence holds needs none, and that
+  // sequence, if the batch lists it, still finds itself the last one.
+  void hold_source(int64_t src, std::vector<int64_t>& held) {
+    if (src < 0 || refcount[src] != 1 || !nodes.count(src)) return;
+    ref(src);
+    held.push_back(src);
+  }
+  void drop_held(const std::vector<int64_t>& held) {
+    for (int64_t b : held) unref(b);
+  }
+
   // Records the token taken by take_block: its slot, its id, and the block
   // it fills joins the prefix cache.
   void commit_token(Seq& s, int32_t token, int64_t* slot) {
@@ -380,16 +397,20 @@ int32_t pa_bm_append_tokens(pa_block_manager* bm, const int64_t* seq_ids, const 
   // which the count above took as reclaimable, so no row may fill the cache
   // before every block of the batch is taken.
   int32_t pairs = 0;
+  std::vector<int64_t> held;
+  held.reserve(static_cast<size_t>(n));
   for (int32_t i = 0; i < n; ++i) {
     int32_t src = -1, dst = -1;
     if (bm->take_block(*rows[static_cast<size_t>(i)], &src, &dst) != PA_BM_OK)
       return PA_BM_ERR_NO_BLOCKS;  // not reached: the blocks were counted above
+    bm->hold_source(src, held);
     if (src >= 0) {
       cow_pairs[2 * pairs] = src;
       cow_pairs[2 * pairs + 1] = dst;
       ++pairs;
     }
   }
+  bm->drop_held(held);
   for (int32_t i = 0; i < n; ++i)
     bm->commit_token(*rows[static_cast<size_t>(i)], tokens[i], &slots[i]);
   *num_pairs = pairs;
@@ -440,12 +461,15 @@ int32_t pa_bm_append_chunks(pa_block_manager* bm, const int64_t* seq_ids, const 
       s.blocks.reserve(s.blocks.size() + static_cast<size_t>(counts[i] / bs) + 2);
     }
     int32_t pairs = 0;
+    std::vector<int64_t> held;
+    held.reserve(static_cast<size_t>(n));
     for (int32_t i = 0; i < n; ++i) {
       Seq& s = *rows[static_cast<size_t>(i)];
       if (counts[i] == 0) continue;
       int32_t src = -1, dst = -1;
       if (bm->take_block(s, &src, &dst) != PA_BM_OK)
         return PA_BM_ERR_NO_BLOCKS;  // not reached: the blocks were counted above
+      bm->hold_source(src, held);
       if (src >= 0) {
         cow_pairs[2 * pairs] = src;
         cow_pairs[2 * pairs + 1] = dst;
@@ -458,6 +482,7 @@ int32_t pa_bm_append_chunks(pa_block_manager* bm, const int64_t* seq_ids, const 
         bm->changed(s);
       }
     }
+    bm->drop_held(held);
     int64_t at = 0;
     for (int32_t i = 0; i < n; ++i) {
       Seq& s = *rows[static_cast<size_t>(i)];

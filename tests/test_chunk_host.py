@@ -348,6 +348,129 @@ def test_drafts_kept_and_dropped_at_random(seed):
     assert bm.num_free_blocks + bm.num_cached_blocks == nb
 
 
+@pytest.mark.parametrize("how", ["chunks", "tokens"])
+def test_a_copy_source_is_not_handed_out_in_its_batch(how):
+    """Sequences cut inside a cached block copy it on the next append; the first one's source is
+    then held by the cache alone, and the pool has no other block for the second one's copy but
+    the one the third sequence left."""
+    bm = BlockManager(4, 4, True)
+    for sid in (1, 2, 3):
+        bm.add_sequence(sid, [])
+        bm.append_chunks([sid], [[10 * sid + i for i in range(4)]])
+    bm.free_sequence(3)
+    bm.keep([1, 2], [3, 3])
+    old = [int(bm.slots(s, 0, 1)[0]) // 4 for s in (1, 2)]
+    if how == "chunks":
+        slots, pairs = bm.append_chunks([1, 2], [[40], [80]])
+    else:
+        slots, pairs = bm.append_tokens([1, 2], [40, 80])
+    assert [p[0] for p in pairs.tolist()] == old and len({int(p[1]) for p in pairs}) == 2
+    assert not {int(p[0]) for p in pairs} & {int(p[1]) for p in pairs}
+    assert [int(s) // 4 for s in slots] == [int(p[1]) for p in pairs]
+    # the sources are evictable again: the pool still serves two more blocks
+    bm.free_sequence(2)
+    bm.add_sequence(9, [1] * 12)
+
+
+@pytest.mark.parametrize("how", ["chunks", "tokens"])
+def test_sharers_of_a_held_block_still_write_in_place(how):
+    """Three sequences share a partial block: two copy it, the last one writes in place."""
+    bm = BlockManager(8, 4, True)
+    bm.add_sequence(1, [1, 2])
+    bm.fork(1, 2)
+    bm.fork(1, 3)
+    at = int(bm.slots(1, 0, 1)[0]) // 4
+    slots, pairs = (bm.append_chunks([1, 2, 3], [[5], [6], [7]]) if how == "chunks"
+                    else bm.append_tokens([1, 2, 3], [5, 6, 7]))
+    assert len(pairs) == 2 and int(slots[2]) // 4 == at
+    assert not {int(p[0]) for p in pairs} & {int(p[1]) for p in pairs}
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_keep_and_eviction_at_random(seed):
+    """Random chunks, single steps, cuts, forks and new prompts in a pool that runs out: every
+    sequence's tokens stay those of a plain model, the copies of a batch are applied all at once
+    (no block is a source of one and the destination of another), and a refused call changes
+    nothing."""
+    rng = random.Random(seed)
+    bs, nb = 4, 14
+    bm = BlockManager(nb, bs, True)
+    model, cells, nxt, copies, refused = {}, {}, 0, 0, 0
+
+    def check():
+        for sid, toks in model.items():
+            assert bm.length(sid) == len(toks)
+            for j, s in enumerate(bm.slots(sid, 0, len(toks))):
+                assert cells[int(s)] == tuple(toks[:j + 1]), (sid, j)
+
+    for step in range(300):
+        what = rng.random()
+        if what < 0.2 or not model:
+            toks = [rng.randint(0, 1) for _ in range(rng.randint(1, 9))]
+            try:
+                cached = bm.add_sequence(nxt, toks)
+            except BlockManagerError as e:
+                assert e.code == ERR_NO_BLOCKS
+                refused += 1
+                if model:
+                    sid = rng.choice(list(model))
+                    bm.free_sequence(sid)
+                    del model[sid]
+                continue
+            model[nxt] = toks
+            for j, s in enumerate(bm.slots(nxt, cached, len(toks) - cached)):
+                cells[int(s)] = tuple(toks[:cached + j + 1])
+            nxt += 1
+        elif what < 0.28:
+            sid = rng.choice(list(model))
+            bm.fork(sid, nxt)
+            model[nxt] = list(model[sid])
+            nxt += 1
+        elif what < 0.4:
+            sid = rng.choice(list(model))
+            bm.free_sequence(sid)
+            del model[sid]
+        elif what < 0.6:
+            ids = rng.sample(list(model), rng.randint(1, len(model)))
+            keep = [rng.randint(max(0, len(model[s]) - 5), len(model[s])) for s in ids]
+            bm.keep(ids, keep)
+            for s, n in zip(ids, keep):
+                del model[s][n:]
+        else:
+            ids = rng.sample(list(model), rng.randint(1, len(model)))
+            single = rng.random() < 0.4
+            lists = [[rng.randint(0, 1) for _ in range(1 if single else rng.randint(0, 5))]
+                     for _ in ids]
+            try:
+                if single:
+                    slots, pairs = bm.append_tokens(ids, [r[0] for r in lists])
+                else:
+                    slots, pairs = bm.append_chunks(ids, lists, offer=rng.random() < 0.5)
+            except BlockManagerError as e:
+                assert e.code == ERR_NO_BLOCKS
+                refused += 1
+                check()
+                continue
+            copies += len(pairs)
+            dst = [int(p[1]) for p in pairs]
+            assert len(set(dst)) == len(dst) and not set(dst) & {int(p[0]) for p in pairs}
+            for s, d in pairs:
+                for r in range(bs):
+                    if s * bs + r in cells:
+                        cells[int(d) * bs + r] = cells[int(s) * bs + r]
+            at = 0
+            for sid, run in zip(ids, lists):
+                for t in run:
+                    model[sid].append(t)
+                    cells[int(slots[at])] = tuple(model[sid])
+                    at += 1
+        check()
+    assert copies > 0 and refused > 0
+    for sid in list(model):
+        bm.free_sequence(sid)
+    assert bm.num_free_blocks + bm.num_cached_blocks == nb
+
+
 def test_refused_drafts_are_not_cached():
     bm = BlockManager(32, 4, True)
     bm.add_sequence(1, [1, 2, 3])
