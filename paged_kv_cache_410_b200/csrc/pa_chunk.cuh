@@ -231,6 +231,14 @@ struct ChunkCfg {
   static constexpr int kFit = (kBudget - NT * kQTile - kRawStages * kRaw) / kBuf;
   static constexpr int kBufs = kFit < 10 ? kFit : 10;
   static_assert(kBufs >= 3, "a K and a V step in use and one arriving");
+  // Barriers of the ring: buffer n's use is phase n / kBars of barrier
+  // n % kBars. kBars is even, so that a barrier serves K or V alone also where
+  // an odd ring lets them share buffers: whoever waits for one has waited for
+  // each of its earlier phases (a parity wait takes the phase before last for
+  // its own otherwise: two producers that take turns on one barrier skip every
+  // second phase).
+  static constexpr int kBars = kBufs % 2 ? 2 * kBufs : kBufs;
+  static_assert(kBars <= 10, "room for the barriers");
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + NT * kQTile;
   static constexpr int kRawOff = kRing + kBufs * kBuf;
@@ -356,6 +364,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   constexpr int BN = C::BN;
   constexpr int SLABS = C::kSlabs;
   constexpr int NBUF = C::kBufs;
+  constexpr int NBAR = C::kBars;
   constexpr uint32_t kIdescS = umma_idesc<BF16, BN, false>();
   constexpr uint32_t kIdescPV = umma_idesc<BF16, D, true>();
 
@@ -367,8 +376,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
     if (threadIdx.x == 0) flag_error(PA_DEVERR_TIMEOUT);
     return;
   }
-  const uint32_t bar_full = small;            // + 8 * buffer (<= 10)
-  const uint32_t bar_free = small + 80;       // + 8 * buffer
+  const uint32_t bar_full = small;            // + 8 * (buffer's use % NBAR)
+  const uint32_t bar_free = small + 80;       // + 8 * (buffer's use % NBAR)
   const uint32_t bar_s = small + 160;         // + 16 * tile + 8 * S buffer
   const uint32_t bar_p = small + 192;         // + 16 * tile + 8 * S buffer
   const uint32_t bar_pv = small + 272;        // + 16 * tile + 8 * S buffer
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   if (NT == 2 && lane == 0 && warp < C::kSoftmaxWarps)
     asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(s_live + 4 * warp), "r"(warp_live ? 1u : 0u) : "memory");
   if (tid == C::kSWarp * 32) {
-    for (int i = 0; i < NBUF; ++i) {
+    for (int i = 0; i < NBAR; ++i) {
       mbar_init(bar_full + 8 * i, MODE == kChunkTma ? 1 : C::kLoadWarps);
       mbar_init(bar_free + 8 * i, NT);
     }
@@ -475,9 +484,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(tmem) : "r"(tmem_slot));
   bool ok = true;
-  // buffer n of the ring (K of step it: n = 2 it, V: 2 it + 1)
+  // use n of the ring (K of step it: n = 2 it, V: 2 it + 1): its buffer, its
+  // barriers, their phase, and the wait for the use before it to end
   auto buf = [&](int n) { return sRing + static_cast<uint32_t>(n % NBUF) * C::kBuf; };
-  auto parity = [](int n) { return static_cast<uint32_t>((n / NBUF) & 1); };
+  auto full_of = [&](int n) { return bar_full + 8 * (n % NBAR); };
+  auto parity = [](int n) { return static_cast<uint32_t>((n / NBAR) & 1); };
+  auto wait_free = [&](int n) {
+    return n < NBUF || chunk_wait(bar_free + 8 * ((n - NBUF) % NBAR), parity(n - NBUF), abort);
+  };
   const int32_t* table = p.block_tables + static_cast<int64_t>(ct.b) * p.max_blocks_per_seq;
   auto block_of = [&](int j) -> int {  // physical block of token j, -1 if out of range
     const int id = __ldg(table + (j >> p.bs_log2));
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           if (z_hi < BN || z_lo > 0) {
             const int n = 2 * it + 1;
             ok = __all_sync(0xffffffffu,
-                            chunk_wait(bar_full + 8 * (n % NBUF), parity(n), abort));
+                            chunk_wait(full_of(n), parity(n), abort));
             if (!ok) return false;
             for (int i = my_row; i < BN * SLABS * 8; i += 128) {
               const int r = i >> 3 & (BN - 1);
@@ -816,9 +830,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           }
         }
       };
-      auto wait_free = [&](int n) {
-        return n < NBUF || chunk_wait(bar_free + 8 * (n % NBUF), parity(n - NBUF), abort);
-      };
       // finish a step whose copies (this thread's own) have landed
       auto finish = [&](int it) -> bool {
 #pragma unroll
@@ -856,7 +867,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           }
           fence_async_smem();
           __syncwarp();
-          mbar_arrive_by(lane == 0, bar_full + 8 * (n % NBUF));
+          mbar_arrive_by(lane == 0, full_of(n));
         }
         return true;
       };
@@ -899,23 +910,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
         // as V (MN-major); offsets add in 16-byte units
         const uint64_t dq = sw128_desc(sQ + t * C::kQTile, 16, 1024);
         const uint64_t dkv = is_s ? sw128_desc(sRing, 16, 1024) : sw128_desc(sRing, C::kBufSlab, 1024);
-        // ring position: K of step i is buffer 2 i, V 2 i + 1
+        // this step's use of the ring, modulo NBAR
         int slot = is_s ? 0 : 1;
         uint32_t phase = 0;
         if (is_s) ok = chunk_wait(bar_q, 0, abort);
         // (a parity wait tells a phase from the one before or after only; so
         // every barrier here is waited for when its last phase but one is known
-        // to be over and its next cannot end yet. With an odd ring K and V share
-        // slots, and only P.V(it - 2), waited for first, says that V(it - 2) has
-        // been there: no asking ahead.)
-        constexpr bool kAsk = NBUF % 2 == 0;
+        // to be over and its next cannot end yet)
         bool ready = false;  // asked ahead whether the buffer is full
         for (int it = 0; ok && it < nsteps; ++it) {
           const bool mine = it >= a && it < b;
           const uint32_t i = (it - a) & 1, ph = ((it - a) >> 1) & 1;
-          if (kAsk && !ready) ready = mbar_test(bar_full + 8 * slot, phase);
-          if (kAsk && is_s && !(ok = ready || chunk_wait(bar_full + 8 * slot, phase, abort))) break;
-          ready = ready || (kAsk && is_s);
+          if (!ready) ready = mbar_test(bar_full + 8 * slot, phase);
+          if (is_s && !(ok = ready || chunk_wait(bar_full + 8 * slot, phase, abort))) break;
+          ready = ready || is_s;
           if (mine) {
             // S: the buffer's last P has been read; P.V: P is there
             if (is_s)
@@ -925,10 +933,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           }
           if (!ok || !(ok = ready || chunk_wait(bar_full + 8 * slot, phase, abort))) break;
           const uint32_t free_bar = bar_free + 8 * slot;
-          const uint64_t dst = dkv + static_cast<uint32_t>(slot * (C::kBuf >> 4));
+          const int at = NBAR > NBUF && slot >= NBUF ? slot - NBUF : slot;
+          const uint64_t dst = dkv + static_cast<uint32_t>(at * (C::kBuf >> 4));
           slot += 2;
-          if (slot >= NBUF) {
-            slot -= NBUF;
+          if (slot >= NBAR) {
+            slot -= NBAR;
             phase ^= 1;
           }
           tc_fence_after();
@@ -949,7 +958,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
             umma_commit(free_bar);
           }
           __syncwarp();
-          ready = kAsk && it + 1 < nsteps && mbar_test(bar_full + 8 * slot, phase);
+          ready = it + 1 < nsteps && mbar_test(bar_full + 8 * slot, phase);
         }
         // every issued MMA has completed before TMEM is released
         if (lane == 0) umma_commit(bar_done);
@@ -983,22 +992,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
       for (int it = 0; it < nsteps; ++it) {
         const int next = it + 1 < nsteps ? slot_of(it + 1) : 0;
         const int n = 2 * it + kv;
-        if (n >= NBUF && !__all_sync(0xffffffffu, chunk_wait(bar_free + 8 * (n % NBUF),
-                                                              parity(n - NBUF), abort)))
-          break;
-        const uint32_t bar = bar_full + 8 * (n % NBUF);
+        if (!__all_sync(0xffffffffu, wait_free(n))) break;
+        const uint32_t bar = full_of(n);
         mbar_arrive_expect_tx_by(lane == 0, bar, C::kBuf);
         __syncwarp();
         if (lane < nbox) tma_load_3d(buf(n) + sl * C::kBufSlab + u0 * 128, map, bar, sl * 64, hk, slot);
         issued = it + 1;
         slot = next;
       }
-      // every issued copy has landed before the CTA can exit: those of the last
-      // NBUF buffers (an earlier one's barrier has gone on to a later buffer)
+      // every issued copy has landed before the CTA can exit: the last one of
+      // each barrier (the last copy's wait for its buffer says that those
+      // before have)
       if (lane == 0)
-        for (int it = max(issued - (NBUF + 1) / 2, 0); it < issued; ++it)
-          if (2 * it + kv >= 2 * issued - NBUF)
-            mbar_wait(bar_full + 8 * ((2 * it + kv) % NBUF), parity(2 * it + kv));
+        for (int it = max(issued - NBAR / 2, 0); it < issued; ++it)
+          mbar_wait(full_of(2 * it + kv), parity(2 * it + kv));
       if (kv == 0) drain_q();
     }
   }
