@@ -91,7 +91,8 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2, PA_F32 = 3 } pa_dt
 #define PA_DEVERR_PROBS 0x80u    /* pa_verify_draft: a row of probabilities without a positive,
                                       finite value */
 #define PA_DEVERR_TIMEOUT 0x10u    /* a kernel's bounded wait for its own tensor-core
-                                      work gave up (1 s); its results are not written */
+                                      work gave up (1 s); its results are not written (those of
+                                      a pa_attend_chunk that splits contexts are undefined) */
 
 /* Describes one paged KV cache (one layer's K cache and V cache). */
 typedef struct pa_cache_desc {
@@ -302,6 +303,14 @@ pa_status pa_copy_blocks_layers(const int32_t* pairs_host, int32_t num_pairs,
  * error word gets PA_DEVERR_TIMEOUT; the context stays usable. Off by
  * default; not for production calls. */
 void pa_testing_withhold_prefix_scores(int32_t on);
+
+/* Test hook for the failure path of pa_attend_chunk. While `tiles` is not 0
+ * (process-wide), its kernel does not issue the scores of row tile 0 (bit 0)
+ * or 1 (bit 1) of a CTA: the waits for them run out after their 1 s limit,
+ * every role of the CTA drains, no row of a chunk that is not split is
+ * written and the device error word gets PA_DEVERR_TIMEOUT; the context stays
+ * usable. 0 by default; not for production calls. */
+void pa_testing_withhold_chunk_scores(int32_t tiles);
 
 /* Test hook for the failure path of a steal-mode decode that merges its rows
  * inside the launch (see pa_set_deterministic: a single long sequence whose

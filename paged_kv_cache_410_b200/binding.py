@@ -33,6 +33,7 @@ EXPORTED = ["pa_append_kv", "pa_decode_workspace_size", "pa_decode_partition_tok
             "pa_decode_sliding_window_workspace_size", "pa_decode_sliding_window",
             "pa_append_decode", "pa_copy_blocks_layers",
             "pa_decode_shared_prefix_partition_tokens", "pa_testing_withhold_prefix_scores",
+            "pa_testing_withhold_chunk_scores",
             "pa_set_deterministic", "pa_testing_withhold_steal_counts",
             "pa_decode_partial", "pa_merge_partials", "pa_attend_chunk_workspace_size",
             "pa_attend_chunk", "pa_verify_draft", "pa_calibrate_kv", "pa_gather_kv"]
@@ -115,6 +116,8 @@ def load_library(path: str = LIB_PATH):
     lib.pa_decode_shared_prefix_partition_tokens.restype = i32
     lib.pa_testing_withhold_prefix_scores.argtypes = [i32]
     lib.pa_testing_withhold_prefix_scores.restype = None
+    lib.pa_testing_withhold_chunk_scores.argtypes = [i32]
+    lib.pa_testing_withhold_chunk_scores.restype = None
     lib.pa_attend_chunk_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i32, D]
     lib.pa_attend_chunk_workspace_size.restype = ctypes.c_size_t
     lib.pa_attend_chunk.argtypes = [P, i32, i64, i32, i32, P, P, D, P, i32, P, i32, P, i32, i32,
@@ -589,6 +592,13 @@ def pa_testing_withhold_prefix_scores(on: bool):
     """Test hook (process-wide): the shared-prefix tensor-core kernel's MMA
     warp issues nothing, so its bounded waits run out (PA_DEVERR_TIMEOUT)."""
     load_library().pa_testing_withhold_prefix_scores(1 if on else 0)
+
+
+def pa_testing_withhold_chunk_scores(tiles: int):
+    """Test hook (process-wide): the chunk kernel does not issue the scores of
+    row tile 0 (bit 0) or 1 (bit 1) of a CTA, so its bounded waits run out
+    (PA_DEVERR_TIMEOUT); 0 turns it off."""
+    load_library().pa_testing_withhold_chunk_scores(int(tiles))
 
 
 def pa_get_device_error(stream=None) -> int:

@@ -697,6 +697,7 @@ pa_status launch_cascade_t(const pa::DecodeParams& p, const CascadePlan& pl, cud
 
 std::mutex g_hook_mu;
 int g_withhold_prefix_scores = 0;  // pa_testing_withhold_prefix_scores
+std::atomic<int> g_withhold_chunk_scores{0};  // pa_testing_withhold_chunk_scores
 
 // 16-bit caches: the tcgen05 prefix kernel, then the suffix decode (cascade
 // mode) as its programmatic dependent, so that the two run side by side
@@ -1122,6 +1123,7 @@ pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, in
   p.window = window;
   p.num_slots = static_cast<int>(
       std::min<int64_t>(cache->num_blocks * cache->block_size, 0x7fffffff));
+  p.withhold_scores = g_withhold_chunk_scores.load(std::memory_order_relaxed);
   p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * 1.4426950408889634f;
   p.sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
   return q_dtype == PA_F16 ? launch_chunk<__half>(p, pl, cache, as_stream(stream))
@@ -1300,6 +1302,10 @@ void pa_testing_withhold_steal_counts(int32_t on) {
 
 int32_t pa_set_deterministic(int32_t on) {
   return g_deterministic.exchange(on != 0 ? 1 : 0);
+}
+
+void pa_testing_withhold_chunk_scores(int32_t tiles) {
+  g_withhold_chunk_scores.store(tiles & 3, std::memory_order_relaxed);
 }
 
 void pa_testing_withhold_prefix_scores(int32_t on) {

@@ -91,6 +91,7 @@ struct ChunkParams {
   int max_context;
   int window;                 // 0: the whole history
   int num_slots;              // TMA: a slot past the map (loads zeros)
+  int withhold_scores;        // test hook: row tiles (one bit each) whose S is not issued
   float scale_log2;           // |scale| * log2(e)
   float sign;                 // 1, -1 or 0: the sign of scale
 };
@@ -590,10 +591,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
     // the same scheduler. In step they would use each pipe at the same time and
     // leave the others idle; in turn one computes its exponentials while the
     // other loads its scores, finds their maximum and stores P. Steps that both
-    // tiles have, where both warps have rows; tile 0 starts. A warp that gives up
-    // hands the turn on once, and the other sees the abort flag before it waits
-    // for another.
+    // tiles have, where both warps have rows; tile 0 starts. bar.sync has no limit
+    // of its own: what bounds it is that both warps take all their turns, also one
+    // whose other, bounded waits have failed (it takes the rest empty-handed,
+    // below), so each is waited for by one that comes. (Turns on mbarriers or
+    // polled flags, each wait with its limit: prompts 150 -> 160 us, 968 -> 1095 us.)
     int turn_a = 0, turn_b = 0;
+    int next_turn = 0;  // the step of the next turn to take
     const int my_turn = 1 + tile * 4 + (warp & 3), other_turn = 1 + (tile ^ 1) * 4 + (warp & 3);
     if constexpr (NT == 2) {
       uint32_t other;
@@ -601,6 +605,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
       if (ntiles == 2 && warp_live && other) {
         turn_a = max(tile_a(0), tile_a(1));
         turn_b = min(tile_b(0), tile_b(1));
+        next_turn = turn_a;
         if (tile == 1 && turn_a < turn_b)
           asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
       }
@@ -692,19 +697,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
         };
         // the exponentials of the two tiles' warps of one scheduler take turns
         const bool turn = it >= turn_a && it < turn_b;
-        if (turn) {
-          uint32_t gone;
-          asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort));
-          if (gone) {
-            ok = false;
-            break;
-          }
-          asm volatile("bar.sync %0, 64;\n" ::"r"(my_turn) : "memory");
-        }
+        if (turn) asm volatile("bar.sync %0, 64;\n" ::"r"(my_turn) : "memory");
         exp32(0, s0);
         exp32(32, s1);
         if (turn && (tile == 0 || it + 1 < turn_b))
           asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
+        if (turn) next_turn = it + 1;
         const float2 t2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
         l_run = l_run * alpha + (t2.x + t2.y);
         m_run = m_ref;
@@ -736,7 +734,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
       __syncwarp();
       mbar_arrive_by(lane == 0, bar_p + 16 * tile + 8 * ((it - a) & 1));
     }
-    if (!ok && turn_a < turn_b) asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
+    if (!ok)
+      for (; next_turn < turn_b; ++next_turn) {  // the turns of the steps given up
+        asm volatile("bar.sync %0, 64;\n" ::"r"(my_turn) : "memory");
+        if (tile == 0 || next_turn + 1 < turn_b)
+          asm volatile("bar.arrive %0, 64;\n" ::"r"(other_turn) : "memory");
+      }
     if (ok && b > a) {  // the last P.V
       const int n = b - a - 1;
       ok = __all_sync(0xffffffffu, chunk_wait(bar_pv + 16 * tile + 8 * (n & 1),
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
         // this step's use of the ring, modulo NBAR
         int slot = is_s ? 0 : 1;
         uint32_t phase = 0;
-        if (is_s) ok = chunk_wait(bar_q, 0, abort);
+        if (is_s) ok = chunk_wait(bar_q, 0, abort) && !(p.withhold_scores >> t & 1);
         // (a parity wait tells a phase from the one before or after only; so
         // every barrier here is waited for when its last phase but one is known
         // to be over and its next cannot end yet)

@@ -279,3 +279,50 @@ def test_device_bounds_are_reported_not_faulted():
         out, err = run(cu=torch.tensor(cu, dtype=torch.int32))
         assert err & B.DEVERR_CHUNK, cu
         assert torch.equal(out[9:], c["out"][9:]) or cu[-1] > 9
+
+
+@pytest.mark.parametrize("layout", [
+    (2, 2, 128, 16, BF16, "io"), (2, 1, 64, 16, F16, "io"), (2, 1, 128, 4, F16, "io"),
+    (2, 2, 128, 16, F16, "e4m3"),
+], ids=str)
+@pytest.mark.parametrize("chunks,tiles", [([5, 60], 1), ([200, 40], 1), ([200, 40], 2), ([200, 40], 3)],
+                         ids=str)
+def test_waits_that_run_out_are_reported_and_recoverable(layout, chunks, tiles):
+    """Scores of a row tile withheld (the test hook): its softmax warps' waits run out, the other
+    tile's warps give up wherever they are (some of them in their turns), nothing is written,
+    the error word says so and the next call is right."""
+    hq, hkv, d, bs, dtype, kind = layout
+    c = chunk_case(2, hq, hkv, d, bs, dtype, chunks, [700, 130], kind, seed=5)
+    g = on_gpu(c)
+    part = 1024                                        # one partition: nothing is merged
+    before = g["out"].clone()
+    B.pa_testing_withhold_chunk_scores(tiles)
+    try:
+        out = call(g, partition_tokens=part)
+        torch.cuda.synchronize()
+        assert B.pa_get_device_error() == B.DEVERR_TIMEOUT
+    finally:
+        B.pa_testing_withhold_chunk_scores(0)
+    # (a CTA whose only tile is not withheld is done as ever)
+    rows = slice(0, 128 // (hq // hkv)) if tiles & 1 else slice(0, 0)
+    assert torch.equal(out[rows][:chunks[0]], before[rows][:chunks[0]])
+    got = call(g, partition_tokens=part)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error() == 0
+    check(c, got)
+
+
+def test_waits_that_run_out_in_a_split_context():
+    c = chunk_case(1, 4, 2, 64, 16, F16, [3], [900], seed=6)
+    g = on_gpu(c)
+    B.pa_testing_withhold_chunk_scores(1)
+    try:
+        call(g, partition_tokens=128)
+        torch.cuda.synchronize()
+        assert B.pa_get_device_error() == B.DEVERR_TIMEOUT
+    finally:
+        B.pa_testing_withhold_chunk_scores(0)
+    got = call(g, partition_tokens=128)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error() == 0
+    check(c, got)
