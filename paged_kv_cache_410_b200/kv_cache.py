@@ -395,16 +395,19 @@ class PagedKVCache:
         under other scales keep their codes."""
         if not self.e4m3:
             raise ValueError("only an E4M3 cache has scales")
+        c = self.layers[layer]
         with self._on_stream():
             if self._amax[layer] is None:
-                new = lambda: torch.zeros((self.num_kv_heads, self.head_dim),  # noqa: E731
-                                          dtype=torch.float32, device=self.device)
-                self._amax[layer] = (new(), new())
-                c = self.layers[layer]
-                c.k_scale, c.v_scale, c.k_inv_scale, c.v_inv_scale = new(), new(), new(), new()
-            c = self.layers[layer]
-            B.pa_calibrate_kv(k, v, slot_mapping, *self._amax[layer], c.k_scale, c.v_scale,
-                              c.k_inv_scale, c.v_inv_scale, self.stream)
+                amax, scales = ([torch.zeros((self.num_kv_heads, self.head_dim),
+                                             dtype=torch.float32, device=self.device)
+                                 for _ in range(n)] for n in (2, 4))
+            else:
+                amax = self._amax[layer]
+                scales = (c.k_scale, c.v_scale, c.k_inv_scale, c.v_inv_scale)
+            # (a refused call raises here and leaves the layer its scales)
+            B.pa_calibrate_kv(k, v, slot_mapping, *amax, *scales, self.stream)
+        self._amax[layer] = amax
+        c.k_scale, c.v_scale, c.k_inv_scale, c.v_inv_scale = scales
 
     def _check_lockstep(self, slots, pairs, lens):
         import torch.distributed as dist

@@ -545,6 +545,33 @@ def test_read_and_calibrate_calls(rec):
         plain.calibrate(0, x, x)
 
 
+def test_a_refused_calibration_leaves_the_scales(rec):
+    twos = [torch.full((2, 64), 2.0)]
+    c = PagedKVCache(64, 4, 2, 64, dtype=torch.uint8, io_dtype=torch.float16, device="cpu",
+                     max_blocks_per_seq=16, stream=0, k_scales=twos, v_scales=twos)
+    x = torch.zeros((3, 2, 64), dtype=torch.float16)
+    bad = [(x[:, :1], x, None), (x, x[:2], None), (x.float(), x, None), (x, x.bfloat16(), None),
+           (x.transpose(1, 2), x, None), (x, x, i32(3)), (x, x, torch.zeros(2, dtype=torch.int64))]
+    layer = c.layers[0]
+
+    def scales():
+        return layer.k_scale, layer.v_scale, layer.k_inv_scale, layer.v_inv_scale
+
+    before = scales()
+    for args in bad:
+        with pytest.raises((ValueError, TypeError)):
+            c.calibrate(0, *args)
+        assert all(a is b for a, b in zip(scales(), before)) and c._amax[0] is None
+    assert bool((layer.k_scale == 2).all()) and bool((layer.k_inv_scale == 0.5).all())
+    c.calibrate(0, x, x)                          # the stub leaves zeros: new arrays are in place
+    after = scales()
+    assert all(a is not b for a, b in zip(after, before))
+    for args in bad:
+        with pytest.raises((ValueError, TypeError)):
+            c.calibrate(0, *args)
+        assert all(a is b for a, b in zip(scales(), after))
+
+
 def test_window_releases_only_what_no_new_token_sees(rec):
     c = PagedKVCache(64, 4, 2, 64, device="cpu", max_blocks_per_seq=32, stream=0, window=6)
     c.add_sequence(0, list(range(20)))
