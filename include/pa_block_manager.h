@@ -101,8 +101,9 @@ int32_t pa_bm_append_tokens(pa_block_manager* bm, const int64_t* seq_ids, const 
  * of these tokens out of the prefix cache until pa_bm_keep: drafts that may
  * be refused. PA_BM_ERR_INVALID for an unknown or repeated id, a negative
  * count or a length past 2^31 - 1, PA_BM_ERR_NO_BLOCKS if the pool cannot
- * supply the batch, PA_BM_ERR_CAPACITY if the host is out of memory; either
- * way nothing has changed. */
+ * supply the batch, PA_BM_ERR_CAPACITY if the host is out of memory; in each
+ * case nothing has changed. (A full block for whose cache entry alone there is
+ * no host memory stays out of the prefix cache.) */
 int32_t pa_bm_append_chunks(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* counts,
                             int32_t n, const int32_t* tokens, int32_t offer, int64_t* slots,
                             int32_t* cow_pairs, int32_t* num_pairs);
@@ -110,8 +111,9 @@ int32_t pa_bm_append_chunks(pa_block_manager* bm, const int64_t* seq_ids, const 
 /* Keep the first lengths[i] tokens of each of n distinct sequences and drop
  * the others (refused drafts): blocks behind them are released, and the full
  * blocks kept are offered to the prefix cache. A length above the sequence's
- * or inside blocks already released (sliding window) is PA_BM_ERR_INVALID;
- * then nothing has changed. */
+ * or inside blocks already released (sliding window) is PA_BM_ERR_INVALID,
+ * PA_BM_ERR_CAPACITY says that the host is out of memory; then nothing has
+ * changed. */
 int32_t pa_bm_keep(pa_block_manager* bm, const int64_t* seq_ids, const int32_t* lengths, int32_t n);
 
 /* child_id starts as a copy of parent_id that shares all its blocks. */

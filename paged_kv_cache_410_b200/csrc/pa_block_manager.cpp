@@ -16,14 +16,19 @@
 
 namespace {
 
+using EvictSet = std::set<std::pair<uint64_t, int64_t>>;  // (last_use, block)
+
 // One cached full block: an edge of the radix tree labelled by the block's
-// block_size token ids, under the node of the block before it.
+// block_size token ids, under the node of the block before it. Its element of
+// the set of evictable blocks is allocated with it and moves in and out, so
+// that references come and go without host memory.
 struct Node {
   int64_t block = -1;
   std::vector<int32_t> tokens;
   Node* parent = nullptr;
   std::unordered_multimap<uint64_t, Node*> children;  // keyed by a hash of the tokens
   uint64_t last_use = 0;
+  EvictSet::node_type outside;  // the set's element while the block is not in it
 };
 
 struct Seq {
@@ -60,7 +65,7 @@ struct pa_block_manager {
   std::unordered_map<int64_t, Seq> seqs;
   Node root;
   std::unordered_map<int64_t, std::unique_ptr<Node>> nodes;  // cached block -> node
-  std::set<std::pair<uint64_t, int64_t>> evictable;           // (last_use, block)
+  EvictSet evictable;
   uint64_t tick = 0;
   uint64_t versions = 0;  // last stamp handed out; stamps are unique across sequences
   uint64_t batches = 0;   // batched calls so far (duplicate ids within one are refused)
@@ -70,17 +75,21 @@ struct pa_block_manager {
   bool is_evictable(const Node* n) const {
     return n->block >= 0 && refcount[n->block] == 1 && n->children.empty();
   }
-  void track(Node* n) {  // keep `evictable` in step with a node's state
-    if (n == &root || !n) return;
-    const auto key = std::make_pair(n->last_use, n->block);
-    if (is_evictable(n))
-      evictable.insert(key);
-    else
-      evictable.erase(key);
+  void take_out(Node* n) noexcept {
+    if (n->outside.empty()) n->outside = evictable.extract(std::make_pair(n->last_use, n->block));
   }
-  void touch(Node* n) {
+  void track(Node* n) noexcept {  // keep `evictable` in step with a node's state
     if (n == &root || !n) return;
-    evictable.erase(std::make_pair(n->last_use, n->block));
+    if (!is_evictable(n)) {
+      take_out(n);
+    } else if (!n->outside.empty()) {
+      n->outside.value() = std::make_pair(n->last_use, n->block);
+      evictable.insert(std::move(n->outside));
+    }
+  }
+  void touch(Node* n) noexcept {
+    if (n == &root || !n) return;
+    take_out(n);
     n->last_use = ++tick;
     track(n);
   }
@@ -144,9 +153,9 @@ struct pa_block_manager {
     return b;
   }
 
-  void unref(int64_t b) {
+  void unref(int64_t b) noexcept {
     if (--refcount[b] == 0) {
-      free_list.push_back(b);
+      free_list.push_back(b);  // (room for every block was reserved)
       return;
     }
     auto it = nodes.find(b);
@@ -235,8 +244,9 @@ struct pa_block_manager {
     return need;
   }
 
-  // Block `index` of `s` is full: extend the cached path with it.
-  void cache_full_block(Seq& s, int32_t index) {
+  // Block `index` of `s` is full: extend the cached path with it. Without host
+  // memory for its node the block stays uncached (and the path ends before it).
+  void cache_full_block(Seq& s, int32_t index) noexcept {
     if (!prefix_cache || s.tail_blocks != index) return;
     Node* parent = s.tail ? s.tail : &root;
     if (index > 0 && !s.tail) return;  // the path was cut by an eviction
@@ -252,14 +262,27 @@ struct pa_block_manager {
       }
     const int64_t blk = s.blocks[index];
     if (nodes.count(blk)) return;  // this block already labels another path
-    auto node = std::make_unique<Node>();
-    node->block = blk;
-    node->tokens.assign(tok, tok + bs);
-    node->parent = parent;
-    node->last_use = ++tick;
-    Node* raw = node.get();
-    parent->children.emplace(h, raw);
-    nodes.emplace(blk, std::move(node));
+    Node* raw = nullptr;
+    try {
+      auto node = std::make_unique<Node>();
+      node->block = blk;
+      node->tokens.assign(tok, tok + bs);
+      node->parent = parent;
+      node->last_use = tick + 1;
+      EvictSet element{std::make_pair(node->last_use, blk)};
+      node->outside = element.extract(element.begin());
+      raw = node.get();
+      const auto child = parent->children.emplace(h, raw);
+      try {
+        nodes.emplace(blk, std::move(node));
+      } catch (...) {
+        parent->children.erase(child);
+        return;
+      }
+    } catch (...) {
+      return;
+    }
+    ++tick;
     ++refcount[blk];  // the cache's own reference
     track(parent);
     track(raw);
