@@ -437,7 +437,8 @@ pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, in
  *   accepted        [batch] int32: accepted drafts a.
  *   tokens          [batch][max_drafts + 1] int32: the a accepted drafts, the
  *                   drawn token, then -1.
- *   max_drafts      host-side upper bound of a sequence's drafts.
+ *   max_drafts      host-side upper bound of a sequence's drafts (vocab and it
+ *                   at most 2^30).
  * A sequence outside its rows or with more than max_drafts drafts sets
  * PA_DEVERR_CHUNK and is left as it was; a token outside the vocabulary sets
  * PA_DEVERR_TOKEN and is refused; a row without weight sets PA_DEVERR_PROBS

@@ -1142,8 +1142,9 @@ pa_status pa_verify_draft(const int32_t* draft_tokens, int64_t num_drafts, int32
   if (!cu_drafts || !target_probs || !sample_uniforms || !accepted || !tokens ||
       (num_drafts > 0 && (!draft_tokens || !accept_uniforms)))
     return PA_ERR_INVALID_ARG;
+  // (token and column indices plus a CTA's stride stay below 2^31)
   if (num_drafts > 0x7fffffffLL || batch > 0x7fffffff / pa::kVerifyMaxCtas ||
-      max_drafts == 0x7fffffff)
+      max_drafts > (1 << 30) || vocab > (1 << 30))
     return PA_ERR_UNSUPPORTED;
   const int64_t size = prob_dtype == PA_F32 ? 4 : 2;
   const uintptr_t addr = reinterpret_cast<uintptr_t>(target_probs) |

@@ -104,6 +104,15 @@ def test_verify_refusals(lib, change, want):
                                None) == want
 
 
+@pytest.mark.parametrize("change", [
+    dict(vocab=(1 << 30) + 1), dict(vocab=0x7fffffff), dict(most=(1 << 30) + 1)])
+def test_verify_refuses_sizes_its_indices_do_not_hold(lib, change):
+    a = dict(vocab=100, most=3)
+    a.update(change)
+    assert lib.pa_verify_draft(P, 6, 2, P, P, P, B.PA_F32, a["vocab"], P, P, a["most"], P, P,
+                               None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("change, want", [
     (dict(t=-1), INVALID), (dict(h=0), INVALID), (dict(d=96), UNSUPPORTED),
     (dict(dt=B.PA_F32), INVALID), (dict(k=None), INVALID), (dict(v=ctypes.c_void_p(8)), INVALID),
