@@ -16,7 +16,10 @@
 // of the one thread that owns the row. P is rounded to the operands' 16 bits
 // (2^-8 or 2^-11 of each weight: what the MMA takes); l sums the weights
 // before that rounding. m moves only when a score passes it by 2^8, so that O
-// is rarely rescaled.
+// is rarely rescaled. With f16 operands m is the maximum less kHeadroom, so that
+// weights use the type's upper range: they lie below 2^15, keep 11 bits down to
+// 2^-21 of the largest and are lost below 2^-32 (of a reference at the maximum
+// itself 2^-14 and 2^-25: a long history behind one large score can weigh as much).
 //
 // K and V steps come through one ring of buffers (K0 V0 K1 V1 ...), filled by
 // two TMA warps (16-bit caches with blocks of 8 tokens or more: whole
@@ -362,6 +365,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   using C = ChunkCfg<D, NT, MODE>;
   // the operands' type: an E4M3 cache is widened to f16, and q folded into it
   constexpr bool BF16 = MODE != kChunkE4m3 && std::is_same<TQ, __nv_bfloat16>::value;
+  constexpr float kHeadroom = BF16 ? 0.f : 7.f;
   constexpr int BN = C::BN;
   constexpr int SLABS = C::kSlabs;
   constexpr int NBUF = C::kBufs;
@@ -675,8 +679,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
         max32(s1, false);
         float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]);
         mx *= scale_log2;
-        const bool up = mx > m_run + kRescaleLog2;  // (the first finite maximum always moves it)
-        const float m_ref = up ? mx : m_run;
+        // (the first finite maximum always moves it)
+        const bool up = mx > m_run + (kHeadroom + kRescaleLog2);
+        const float m_ref = up ? mx - kHeadroom : m_run;
         const float alpha = up ? ex2(m_run - m_ref) : 1.f;
         // a row that has seen no token yet keeps p = 2^(-inf) = 0
         const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;

@@ -1,6 +1,8 @@
 """Chunk attention over the paged cache (pa_attend_chunk) on the GPU, against
 float64 attention row by row (tests/chunk_plain.py, whose docstring derives
 the bound that every value is held to)."""
+import math
+
 import pytest
 import torch
 
@@ -326,3 +328,40 @@ def test_waits_that_run_out_in_a_split_context():
     torch.cuda.synchronize()
     assert B.pa_get_device_error() == 0
     check(c, got)
+
+
+@pytest.mark.parametrize("kind,d,partition_tokens", [
+    ("io", 64, 0), ("io", 128, 512), ("e4m3", 64, 0), ("e4m3", 128, 512)])
+@pytest.mark.parametrize("down", [18.0, 22.0, 26.0])
+def test_a_long_history_behind_one_large_score(kind, d, partition_tokens, down):
+    """One token's score is `down` bits above all others and its V is zero: the row is the sum of
+    2000 small weights. With P in f16 relative to a reference 7 to 15 bits below the maximum, a
+    weight of w (of the largest) is off by at most 2^-11 w or half of f16's smallest step,
+    2^-25 2^-7 = 2^-32: that much of each |v| more than the bound of chunk_plain."""
+    n = 2000
+    c = chunk_case(1, 2, 1, d, 16, F16, [2], [n], kind, seed=8, junk=False)
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1.0
+    sink = 700
+    at = (int(c["tables"][0, sink // 16]), sink % 16)
+    size = down * math.log(2) / c["scale"]              # q.K of the sink, the others' is 0
+    if kind == "e4m3":
+        c["k"].zero_()
+        c["k_scale"].fill_(size / 448)
+        c["k"][at[0], at[1], 0, 0] = 0x7e                # 448
+        c["v"][:] = 0x78                                 # 256
+        c["v_scale"].fill_(0.25)
+    else:
+        c["k"].zero_()
+        c["k"][at[0], at[1], 0, 0] = size
+        c["v"].fill_(64.0)
+    c["v"][at[0], at[1]] = 0
+    got = call(on_gpu(c), partition_tokens=partition_tokens)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error() == 0
+    want, bound = attend_chunk(c["q"], c["k"], c["v"], c["cu"], c["tables"], c["lens"], c["scale"],
+                               c["out"], 0, c["k_scale"], c["v_scale"])
+    assert float(want.abs().min()) > 64 * n * 2.0 ** -(down + 1)
+    bound = bound + n * 64 * 2.0 ** -32
+    assert float(bound.max()) < 0.1 * float(want.abs().min())      # (the bound says something)
+    assert bool(((got.cpu().double() - want).abs() <= bound).all())
