@@ -97,6 +97,21 @@ def test_verify_borders(u, vocab):
     assert got[1] == [[2 * int(u * (vocab // 2))]]
 
 
+def test_verify_low_parts_of_the_differences():
+    """p - q = 1 - 2^-25 and 2^-25 - 2^-50 side by side, then apart: half of the total is reached
+    exactly behind the first two, so the draw is the next token. The first two's low parts, -2^-25
+    and -2^-50, need 26 bits together."""
+    p, q = torch.zeros((2, 12)), torch.zeros((1, 12))
+    for i, j in ((0, 1), (4, 8)):
+        p[0, i], q[0, i] = 1.0, 2.0 ** -25
+        p[0, j], q[0, j] = 2.0 ** -25, 2.0 ** -50
+    x = torch.tensor([2], dtype=torch.int32)             # weightless: refused
+    u = torch.tensor([0.5])
+    want = verify_draft(x, [0, 1], p, q, u, u, 1)
+    assert want == ([0], [[4, -1]])
+    assert run_verify(x, [0, 1], p, q, u, u, 1) == want
+
+
 def test_verify_accept_border_is_strict():
     """u q = p refuses, one step less accepts."""
     target = torch.tensor([[0.25, 0.75], [0.5, 0.5]])
