@@ -459,7 +459,8 @@ def pa_attend_chunk(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, s
     if block_tables.dim() != 2:
         raise ValueError("block_tables: expected [batch, max_blocks_per_seq]")
     batch, hq = block_tables.shape[0], q.shape[1]
-    _on_current(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, out, workspace)
+    _on_current(q, k_cache, v_cache, cu_chunk, block_tables, context_lens, out, workspace,
+                cache.k_scale, cache.v_scale)
     pq = _dev(q, "q", _IO, (q.shape[0], hq, cache.head_dim))
     pt = _dev(block_tables, "block_tables", (torch.int32,))
     pl = _dev(context_lens, "context_lens", (torch.int32,), (batch,))
@@ -541,7 +542,8 @@ def pa_gather_kv(k_cache, v_cache, block_tables, first, cu_tokens, k_out, v_out,
         raise ValueError("block_tables: expected [batch, max_blocks_per_seq]")
     batch, t = block_tables.shape[0], k_out.shape[0]
     shape = (t, cache.num_kv_heads, cache.head_dim)
-    _on_current(k_cache, v_cache, block_tables, first, cu_tokens, k_out, v_out)
+    _on_current(k_cache, v_cache, block_tables, first, cu_tokens, k_out, v_out, cache.k_scale,
+                cache.v_scale)
     i32 = (torch.int32,)
     kc, vc = cache.cache_ptrs(k_cache, v_cache)
     rc = lib.pa_gather_kv(kc, vc, ctypes.byref(d), _dev(block_tables, "block_tables", i32),

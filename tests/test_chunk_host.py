@@ -241,6 +241,29 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
             B._on_current(*bad)
 
 
+def test_scales_of_another_device_are_refused(rec, monkeypatch):
+    """The kernels read the cache's scales: they are among the tensors whose device is checked."""
+    ones = torch.ones((2, 64))
+    k = torch.zeros((8, 16, 2, 64), dtype=torch.uint8)
+    cache = B.PagedCache.for_tensor(k, k_scale=ones, v_scale=ones.clone(), k_inv_scale=ones,
+                                    v_inv_scale=ones)
+    q, kk = torch.zeros((5, 4, 64), dtype=torch.float16), torch.zeros((5, 2, 64), dtype=torch.float16)
+    for bad in (cache.k_scale, cache.v_scale):
+        class Elsewhere(torch.Tensor):
+            def get_device(self):
+                return 1
+
+        kw = {n: (t.as_subclass(Elsewhere) if t is bad else t) for n, t in
+              (("k_scale", cache.k_scale), ("v_scale", cache.v_scale))}
+        other = B.PagedCache.for_tensor(k, k_inv_scale=ones, v_inv_scale=ones, **kw)
+        with pytest.raises(ValueError, match="device"):
+            B.pa_attend_chunk(q, k, k, i32(3), i32(2, 4), i32(2), 1.0, torch.zeros_like(q), other, 3,
+                              20, stream=0)
+        with pytest.raises(ValueError, match="device"):
+            B.pa_gather_kv(k, k, i32(2, 4), i32(2), i32(3), kk, kk, other, stream=0)
+    B.pa_gather_kv(k, k, i32(2, 4), i32(2), i32(3), kk, kk, cache, stream=0)
+
+
 # ---- block manager -------------------------------------------------------------
 def test_chunks_equal_single_appends():
     a, b = BlockManager(64, 4, True), BlockManager(64, 4, True)
