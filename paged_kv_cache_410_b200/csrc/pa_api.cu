@@ -166,7 +166,7 @@ void bind_workspace(pa::DecodeParams& p, const Plan& pl, void* ws) {
 // also prefers the largest shared-memory carveout (228 KB per SM), so that
 // CTAs of the shared-prefix and suffix-decode kernels, which run side by
 // side, find the same split of each SM and fit next to each other.
-cudaError_t ensure_smem(const void* kernel, int bytes) {
+cudaError_t ensure_smem(const void* kernel, int bytes) try {
   static std::mutex mu;
   static std::unordered_map<const void*, std::array<int, 64>> done;
   int dev = 0;
@@ -185,6 +185,8 @@ cudaError_t ensure_smem(const void* kernel, int bytes) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) have = bytes;
   return e;
+} catch (...) {  // (host memory for the map's entry: nothing passes the C entries)
+  return cudaErrorMemoryAllocation;
 }
 
 // Launch `kern` as the programmatic dependent of the kernel before it in
@@ -842,18 +844,16 @@ ChunkPlan make_chunk_plan(int64_t num_tokens, int64_t batch, int64_t num_q_heads
 
 // Whether `kern` was compiled for `regs` registers a thread: its warps move
 // registers between them, and an increase beyond what the launch holds would
-// wait for good.
-bool launches_with(const void* kern, int regs) {
-  static std::mutex mu;
-  static std::unordered_map<const void*, int> have;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = have.find(kern);
-  if (it == have.end()) {
+// wait for good. `have` keeps the kernel's registers (0: not asked yet).
+bool launches_with(const void* kern, int regs, std::atomic<int>& have) {
+  int n = have.load(std::memory_order_relaxed);
+  if (n == 0) {
     cudaFuncAttributes a{};
     if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) return false;
-    it = have.emplace(kern, a.numRegs).first;
+    n = a.numRegs;
+    have.store(n, std::memory_order_relaxed);
   }
-  return (it->second + 7) / 8 * 8 >= regs;
+  return (n + 7) / 8 * 8 >= regs;
 }
 
 template <typename TQ, int D, int NT, int MODE>
@@ -863,7 +863,8 @@ pa_status launch_chunk_t(const pa::ChunkParams& p, const CUtensorMap& tq, const 
   auto kern = pa::pa_chunk_kernel<TQ, D, NT, MODE>;
   if (ensure_smem(reinterpret_cast<const void*>(kern), C::kRequest) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (!launches_with(reinterpret_cast<const void*>(kern), C::kLaunchRegs)) return PA_ERR_CUDA;
+  static std::atomic<int> regs{0};
+  if (!launches_with(reinterpret_cast<const void*>(kern), C::kLaunchRegs, regs)) return PA_ERR_CUDA;
   const int64_t ctas = static_cast<int64_t>(p.num_tiles) * p.num_kv_heads * p.head_blocks *
                        p.num_partitions;
   const dim3 grid(static_cast<unsigned>(ctas));
