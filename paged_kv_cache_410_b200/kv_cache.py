@@ -38,6 +38,14 @@ step:
     accepted, tokens = cache.verify(plan, target_probs, draft_probs, u, u_sample)
     cache.settle(plan, accepted)                         # refused drafts leave the cache
 
+A prompt that ``add_sequence`` placed, with its leading tokens' K/V already
+cached, is attended from the first token that is not (at once or in pieces):
+
+    cached, _ = cache.add_sequence(seq_id, prompt)
+    plan = cache.plan_chunk([seq_id], [cached])
+    for layer in range(num_layers):
+        out = cache.attend_chunk(plan, layer, q, k, v)
+
 ``read`` returns a sequence's cached K/V as contiguous rows, and ``calibrate``
 finds an E4M3 layer's scales from K/V before the cache is first written.
 
@@ -163,7 +171,7 @@ class PagedKVCache:
     def add_sequence(self, seq_id: int, token_ids):
         """Place a prompt. Returns (tokens whose K/V is already cached, int64
         device slots of the others, in order). Store the others' K/V for every
-        layer (store_prompt) before the next add_sequence or step: the prompt's
+        layer (store_prompt, or plan_chunk and attend_chunk) before the next add_sequence or step: the prompt's
         full blocks are offered to later prompts as soon as they exist."""
         cached = self.bm.add_sequence(seq_id, token_ids)
         rest = self.bm.slots(seq_id, cached, len(token_ids) - cached)
@@ -293,22 +301,58 @@ class PagedKVCache:
             # blocks that hold only tokens before the first new token's window
             for s, n, c in zip(ids, lens, counts):
                 self.bm.release_before(int(s), max(0, int(n) - int(c) - self.window + 1))
-        if self.lockstep_group is not None:
-            self._check_lockstep(slots, pairs, lens)
-        cu = np.zeros(len(ids) + 1, dtype=np.int32)
-        np.cumsum(counts, out=cu[1:])
-        cu_drafts = (cu - np.arange(len(ids) + 1)).astype(np.int32) if drafts else None
         later = None
         if drafts:
             later = np.concatenate([np.asarray(t[1:], dtype=np.int32) for t in token_lists]
                                    or [np.zeros(0, np.int32)]).astype(np.int32)
+        return self._upload_chunk(ids, counts, slots, pairs, tables, lens, later)
+
+    def plan_chunk(self, seq_ids, firsts, counts=None, stored=None) -> ChunkPlan:
+        """The plan of tokens that have their places already (a prompt's, after
+        add_sequence): tokens [firsts[i], firsts[i] + counts[i]) of each listed
+        sequence, to its end without `counts`. Their K/V is stored by
+        attend_chunk, but for those before position stored[i], whose K/V is in
+        the cache (a prompt that is cached whole still needs its last row:
+        plan_chunk([s], [n - 1], stored=[n])). A prompt in pieces: one plan
+        after the other, every layer of each, all before the next add_sequence
+        or step; with a window, blocks that no token from firsts[i] on sees
+        return to the pool."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        firsts = np.asarray(firsts, dtype=np.int64)
+        lengths = np.asarray([self.bm.length(int(s)) for s in ids], dtype=np.int64)
+        counts = lengths - firsts if counts is None else np.asarray(counts, dtype=np.int64)
+        stored = firsts if stored is None else np.asarray(stored, dtype=np.int64)
+        if not ids.shape == firsts.shape == counts.shape == stored.shape or ids.ndim != 1:
+            raise ValueError("one first token, count and stored position per sequence")
+        if (firsts < 0).any() or (counts < 0).any() or (firsts + counts > lengths).any():
+            raise ValueError("tokens outside their sequences")
+        runs = [self.bm.slots(int(s), int(f), int(c)) for s, f, c in zip(ids, firsts, counts)]
+        for run, f, p in zip(runs, firsts, stored):
+            run[:max(0, int(p - f))] = -1
+        slots = np.concatenate(runs + [np.zeros(0, np.int64)])
+        tables, _ = self.bm.block_tables(ids, self.max_blocks)
+        if self.window:
+            for s, f in zip(ids, firsts):
+                self.bm.release_before(int(s), max(0, int(f) - self.window + 1))
+        return self._upload_chunk(ids, counts.astype(np.int32), slots,
+                                  np.zeros((0, 2), dtype=np.int32), tables,
+                                  (firsts + counts).astype(np.int32), None)
+
+    def _upload_chunk(self, ids, counts, slots, pairs, tables, lens, drafts) -> ChunkPlan:
+        if self.lockstep_group is not None:
+            self._check_lockstep(slots, pairs, lens)
+        cu = np.zeros(len(ids) + 1, dtype=np.int32)
+        np.cumsum(counts, out=cu[1:])
+        cu_drafts = None
+        if drafts is not None:
+            cu_drafts = (cu - np.arange(len(ids) + 1)).astype(np.int32)
         with self._on_stream():
             up = lambda a: None if a is None else torch.from_numpy(a).to(self.device)  # noqa: E731
             return ChunkPlan(seq_ids=ids, counts=counts, lengths=lens, slot_mapping=up(slots),
                              cu_chunk=up(cu), block_tables=up(tables), context_lens=up(lens),
                              max_chunk=int(counts.max(initial=0)),
                              max_context=int(lens.max(initial=0)), copy_pairs=pairs,
-                             drafts=up(later), cu_drafts=up(cu_drafts))
+                             drafts=up(drafts), cu_drafts=up(cu_drafts))
 
     def attend_chunk(self, plan: ChunkPlan, layer: int, q, k, v, scale: float | None = None,
                      out=None):

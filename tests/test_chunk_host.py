@@ -554,6 +554,53 @@ def test_chunk_plan_and_calls(rec):
     assert [c.bm.length(s) for s in (0, 1, 2)] == [12, 5, 11]
 
 
+def test_plan_of_a_placed_prompt(rec):
+    c = PagedKVCache(64, 4, 2, 64, device="cpu", max_blocks_per_seq=16, stream=0)
+    assert c.add_sequence(0, list(range(10)))[0] == 0
+    cached, slots = c.add_sequence(1, list(range(8)) + [50, 51, 52])
+    assert cached == 8
+    plan = c.plan_chunk([1], [cached])
+    assert plan.slot_mapping.tolist() == slots.tolist() and plan.counts.tolist() == [3]
+    assert plan.context_lens.tolist() == [11] and plan.max_context == 11 and plan.max_chunk == 3
+    assert plan.cu_chunk.tolist() == [0, 3] and plan.drafts is None and len(plan.copy_pairs) == 0
+    assert np.array_equal(plan.block_tables.numpy(), c.bm.block_tables([1], 16)[0])
+    # pieces, beside another sequence's; nothing is reserved by a plan
+    plan = c.plan_chunk([0, 1], [0, 9], [6, 1])
+    assert plan.slot_mapping.tolist() == c.bm.slots(0, 0, 6).tolist() + c.bm.slots(1, 9, 1).tolist()
+    assert plan.context_lens.tolist() == [6, 10] and plan.cu_chunk.tolist() == [0, 6, 7]
+    assert [c.bm.length(s) for s in (0, 1)] == [10, 11]
+    # a prompt cached whole: its last row, whose K/V is not stored again
+    assert c.add_sequence(2, list(range(8)))[0] == 8
+    plan = c.plan_chunk([2, 0], [7, 6], stored=[8, 8])
+    assert plan.slot_mapping.tolist() == [-1, -1, -1] + c.bm.slots(0, 8, 2).tolist()
+    assert plan.context_lens.tolist() == [8, 10]
+    q, k = torch.zeros((5, 4, 64), dtype=torch.float16), torch.zeros((5, 2, 64), dtype=torch.float16)
+    rec.calls.clear()
+    c.attend_chunk(plan, 0, q, k, k)
+    assert [n for n, _ in rec.calls] == ["pa_append_kv", "pa_attend_chunk_workspace_size",
+                                         "pa_attend_chunk"]
+    for bad in (([0], [-1]), ([0], [11]), ([0], [5], [6]), ([0], [5], [-1]), ([0, 1], [5]),
+                ([0], [5], [1, 1]), ([0], [5], [1], [1, 2])):
+        with pytest.raises(ValueError):
+            c.plan_chunk(*bad)
+    with pytest.raises(BlockManagerError):
+        c.plan_chunk([77], [0])
+    assert c.plan_chunk([], []).cu_chunk.tolist() == [0]
+    assert c.plan_chunk([0], [10]).counts.tolist() == [0]
+
+
+def test_plan_of_a_placed_prompt_with_a_window(rec):
+    c = PagedKVCache(64, 4, 2, 64, device="cpu", max_blocks_per_seq=32, stream=0, window=6)
+    c.add_sequence(0, list(range(30)))
+    before = c.plan_chunk([0], [0], [20]).block_tables.clone()
+    assert len(c.bm.slots(0, 0, 30)) == 30
+    plan = c.plan_chunk([0], [20])                # its first row sees 15 .. 20
+    assert torch.equal(plan.block_tables, before)
+    assert len(c.bm.slots(0, 12, 18)) == 18
+    with pytest.raises(BlockManagerError):
+        c.plan_chunk([0], [11])
+
+
 def test_read_and_calibrate_calls(rec):
     ones = [torch.ones((2, 64))]
     c = PagedKVCache(64, 4, 2, 64, dtype=torch.uint8, io_dtype=torch.float16, device="cpu",
