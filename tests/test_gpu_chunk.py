@@ -365,3 +365,31 @@ def test_a_long_history_behind_one_large_score(kind, d, partition_tokens, down):
     bound = bound + n * 64 * 2.0 ** -32
     assert float(bound.max()) < 0.1 * float(want.abs().min())      # (the bound says something)
     assert bool(((got.cpu().double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("kind", ["io", "e4m3"])
+def test_rows_before_the_first_sequence_stay(kind):
+    """cu_chunk may start behind row 0: the rows in front are left as they were."""
+    for chunks, lead in (([3, 0, 5], 7), ([140, 2, 1], 300)):
+        c = chunk_case(3, 4, 2, 64, 16, F16, chunks, [200, 9, 150], kind, seed=12)
+        rows = c["q"].shape[0]
+        g2 = torch.Generator().manual_seed(1)
+        for name in ("q", "out"):
+            c[name] = torch.cat([torch.randn((lead, 4, 64), generator=g2).to(F16), c[name]])
+        c["cu"] = c["cu"] + lead
+        got = call(on_gpu(c))
+        torch.cuda.synchronize()
+        assert B.pa_get_device_error() == 0 and got.shape[0] == rows + lead
+        check(c, got)
+        assert torch.equal(got[:lead].cpu(), c["out"][:lead])
+
+
+def test_no_rows_at_all():
+    c = chunk_case(2, 4, 2, 64, 16, F16, [0, 0], [5, 0], pad=3)
+    c["max_chunk"] = 0
+    got = call(on_gpu(c))
+    assert torch.equal(got.cpu(), c["out"])
+    empty = dict(c, q=c["q"][:0], out=c["out"][:0])
+    assert call(on_gpu(empty)).shape[0] == 0
+    c["max_chunk"] = 4                                    # (an upper bound)
+    assert torch.equal(call(on_gpu(c)).cpu(), c["out"]) and B.pa_get_device_error() == 0
