@@ -399,9 +399,9 @@ size_t pa_attend_chunk_workspace_size(int64_t num_tokens, int32_t batch, int32_t
  * is skipped; a length shorter than the chunk, above max_context or beyond
  * the table sets PA_DEVERR_CONTEXT_LEN and gives zero rows; a bad block id
  * sets PA_DEVERR_BLOCK_ID and its tokens read as zeros.
- * K/V outside a row's tokens never reach it, whatever bits they hold, except
- * that the V of a sequence's own new tokens (and of tokens the window drops
- * within one chunk) must be finite for the rows that do not see them.
+ * K/V outside a row's tokens never reach it, whatever bits they hold. (New
+ * tokens, or tokens that the window drops within one chunk, whose V is not
+ * finite cost the rows that do not see them a second, slow pass.)
  * Results are reproducible: the same inputs, sizes and partition length give
  * the same bits, and any partition length agrees up to rounding. */
 pa_status pa_attend_chunk(const void* q, int32_t q_dtype, int64_t num_tokens, int32_t batch,

@@ -30,7 +30,9 @@
 // What each row may not see is decided by selecting on S, so K of masked
 // tokens never matters; V rows outside the CTA's token range (behind the
 // last row's position, before the first row's window: recycled memory) are
-// zeroed in shared memory, since 0 x NaN would reach the sum.
+// zeroed in shared memory, since 0 x NaN would reach the sum. Inside it a V that
+// is not finite makes every row of the step NaN; rows that do not see it are
+// found by their result and summed again (chunk_unseen_v).
 //
 // What bounds it, measured on one B200 (1.9 GHz, device time):
 //  - drafts (64 requests, 2 to 8 new tokens, 512 to 4096 cached ones, 64 / 8
@@ -247,7 +249,7 @@ struct ChunkCfg {
   static constexpr int kRing = kQ + NT * kQTile;
   static constexpr int kRawOff = kRing + kBufs * kBuf;
   static constexpr int kBytes = kRawOff + kRawStages * kRaw;
-  static constexpr int kSmall = 336;  // barriers, TMEM address, abort flag
+  static constexpr int kSmall = 352;  // barriers, TMEM address, abort flag
   // (the base is 1024-byte aligned as it is: a block's dynamic shared memory
   // starts behind 1 KB of the system's; the kernel checks that the slack holds)
   static constexpr int kSlack = 512;
@@ -355,6 +357,132 @@ __device__ __forceinline__ void set_fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// Eight channels from 8 c of token j's K or V row of KV head hk, widened
+// (zeros for a block outside the cache, as the loads give).
+template <typename TQ, int D, int MODE>
+__device__ __forceinline__ void chunk_row_piece(const ChunkParams& p, const void* cache,
+                                                const int32_t* table, int hk, int j, int c,
+                                                float (&x)[8]) {
+  const int id = __ldg(table + (j >> p.bs_log2));
+  const int64_t slot = (static_cast<int64_t>(id) << p.bs_log2) + (j & ((1 << p.bs_log2) - 1));
+  const int64_t at = (slot * p.num_kv_heads + hk) * D + 8 * c;
+  if (id < 0 || id >= p.num_blocks) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  } else if constexpr (MODE == kChunkE4m3) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at));
+    uint32_t h[4];
+    e4m3x4_to_f16x2x2(w.x, h[0], h[1]);
+    e4m3x4_to_f16x2x2(w.y, h[2], h[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+      x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    }
+  } else {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const TQ*>(cache) + at));
+    const TQ* e8 = reinterpret_cast<const TQ*>(&w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f32<TQ>(e8[e]);
+  }
+}
+
+// P of a token that a row does not see is 0, and 0 x V is NaN where that V is
+// not finite. A row whose result is not finite comes here (never in a run of
+// finite V): the channels in which such a token of the CTA has a V that is not
+// finite are summed again over the tokens the row sees, from its q in shared
+// memory (sQ), and written over. Where the row is comes from what the CTA left in
+// shared memory (`unit`) and the launch: kept in registers through the steps it
+// cost prompts 2 to 4 %.
+// A last token without a finite V costs 2048 rows over 16384 tokens (1.0 ms) 37 ms
+// for one channel, 140 ms for all.
+template <typename TQ, int D, int MODE>
+__device__ __forceinline__ void chunk_unseen_v(const ChunkParams& p, uint32_t unit, uint32_t sQ,
+                                               float scale_log2, float m, float l) {
+  using TO = typename std::conditional<MODE == kChunkE4m3, __half, TQ>::type;
+  uint32_t tid, cta;
+  asm volatile("mov.u32 %0, %%tid.x;\n" : "=r"(tid));
+  asm volatile("mov.u32 %0, %%ctaid.x;\n" : "=r"(cta));
+  int b, row0, pos0, tokens;
+  asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(b), "=r"(row0), "=r"(pos0), "=r"(tokens)
+               : "r"(unit));
+  const int part = cta % p.num_partitions;
+  const int heads_at = cta / p.num_partitions % (p.head_blocks * p.num_kv_heads);
+  const int hk = heads_at / p.head_blocks;
+  const int tile = tid >> 7, my_row = tid & (kUmmaRows - 1), sw = my_row & 7;
+  const int tok = tile * p.tile_tokens + my_row / p.head_rows;
+  const int head = hk * p.group + heads_at % p.head_blocks * p.head_rows + my_row % p.head_rows;
+  const int64_t row = (static_cast<int64_t>(row0) + tok) * p.num_q_heads + head;
+  const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+  // tokens of the CTA in this partition [t0, c1), and of the row [lo, hi]
+  const int cta_lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+  const int c0 = cta_lo / kChunkStep * kChunkStep + part * p.partition_tokens;
+  const int c1 = min(c0 + p.partition_tokens, pos0 + tokens);
+  const int t0 = max(cta_lo, c0);
+  const int lo = max(p.window > 0 ? max(0, pos0 + tok - p.window + 1) : 0, c0);
+  const int hi = min(pos0 + tok, c1 - 1);
+  const uint32_t qrow = sQ + tile * ((D / 64) * kUmmaRows * 128) + my_row * 128;
+  auto put = [&](int d, float x) {
+    if constexpr (MODE == kChunkE4m3) x *= __ldg(p.v_scale + static_cast<int64_t>(hk) * D + d);
+    if (p.num_partitions > 1)
+      p.ws_o[(row * p.num_partitions + part) * D + d] = x;
+    else
+      reinterpret_cast<TQ*>(p.out)[row * D + d] = from_f32<TQ>(x);
+  };
+  uint32_t bad[D / 32] = {};
+  for (int j = t0; j < c1; ++j) {
+    if (j >= lo && j <= hi) {
+      j = hi;
+      continue;
+    }
+#pragma unroll 1
+    for (int c = 0; c < D / 8; ++c) {
+      float x[8];
+      chunk_row_piece<TQ, D, MODE>(p, p.v_cache, table, hk, j, c, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(fabsf(x[e]) < INFINITY)) bad[c >> 2] |= 1u << ((c & 3) * 8 + e);
+    }
+  }
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) any |= bad[i];
+  if (any == 0) return;  // the tokens it sees say so
+  // 32 channels at a time: at most D / 32 passes over the row's K
+#pragma unroll 1
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t mine = bad[i];
+    if (mine == 0) continue;
+    float acc[32] = {};
+#pragma unroll 1
+    for (int j = lo; j <= hi; ++j) {
+      float s = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        float x[8];
+        chunk_row_piece<TQ, D, MODE>(p, p.k_cache, table, hk, j, c, x);
+        const uint4 w = lds128(qrow + (c >> 3) * (kUmmaRows * 128) + (((c & 7) ^ sw) << 4));
+        const TO* q = reinterpret_cast<const TO*>(&w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(to_f32<TO>(q[e]), x[e], s);
+      }
+      if (p.sign != 1.f) s *= p.sign;
+      const float w = ex2(fmaf(s, scale_log2, -m));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float x[8];
+        chunk_row_piece<TQ, D, MODE>(p, p.v_cache, table, hk, j, 4 * i + c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[8 * c + e] = fmaf(w, x[e], acc[8 * c + e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (mine >> e & 1) put(32 * i + e, l != 0.f ? acc[e] / l : 0.f);
+  }
+}
+
 // Grid: tiles x KV heads x head blocks x partitions, partition fastest.
 template <typename TQ, int D, int NT, int MODE>
 __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
@@ -389,6 +517,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
   const uint32_t s_live = small + 304;        // + 4 * softmax warp: whether it has rows
   const uint32_t bar_q = small + 240;
   const uint32_t bar_done = small + 248;
+  const uint32_t unit = small + 336;          // where the CTA's rows are (chunk_unseen_v)
   const uint32_t tmem_slot = small + 264;
   const uint32_t abort = small + 268;
   const uint32_t sQ = base + C::kQ;
@@ -480,6 +609,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
     }
     mbar_init(bar_q, MODE == kChunkE4m3 ? 128 * NT : 1);
     mbar_init(bar_done, 2 * NT);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(unit), "r"(ct.b),
+                 "r"(static_cast<int>(ct.row)), "r"(ct.pos0), "r"(ct.tokens)
+                 : "memory");
     asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(abort), "r"(0u) : "memory");
     mbar_init_fence();
   }
@@ -755,6 +887,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
     if (ok && warp_live && tile < ntiles) {
       const bool any = b > a;
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // no token attended: zeros
+      float finite = 0.f;  // 0 while every value of the row is
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -763,7 +896,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = any && l_run != 0.f ? o[e] * inv : 0.f;
+        for (int e = 0; e < 32; ++e) {
+          o[e] = any && l_run != 0.f ? o[e] * inv : 0.f;
+          finite = fmaf(o[e], 0.f, finite);
+        }
         if constexpr (MODE == kChunkE4m3) {
           const float4* vs = reinterpret_cast<const float4*>(p.v_scale + static_cast<int64_t>(hk) * D + c);
 #pragma unroll
@@ -793,6 +929,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NT, MODE>::kThreads,
           }
         }
       }
+      if (live && finite != 0.f && mbar_wait(bar_q, 0))  // (Q's bytes have landed for this thread)
+        chunk_unseen_v<TQ, D, MODE>(p, unit, sQ, scale_log2, m_run, l_run);
       if (live && p.num_partitions > 1)
         p.ws_ml[row * p.num_partitions + part] = make_float2(m_run, l_run);
     }

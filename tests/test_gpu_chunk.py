@@ -393,3 +393,56 @@ def test_no_rows_at_all():
     assert call(on_gpu(empty)).shape[0] == 0
     c["max_chunk"] = 4                                    # (an upper bound)
     assert torch.equal(call(on_gpu(c)).cpu(), c["out"]) and B.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("layout,bad", [
+    ((2, 2, 128, 16, BF16, "io"), "nan"), ((2, 2, 128, 16, BF16, "io"), "inf"),
+    ((4, 2, 64, 16, F16, "io"), "nan"), ((4, 2, 64, 16, F16, "io"), "-inf"),
+    ((3, 1, 128, 4, F16, "io"), "nan"), ((3, 1, 128, 4, F16, "io"), "inf"),
+    ((2, 1, 128, 16, F16, "e4m3"), "nan"), ((4, 4, 64, 32, BF16, "e4m3"), "nan")], ids=str)
+@pytest.mark.parametrize("chunks,ctxs,window,part", [
+    ([5, 9], [200, 70], 0, 0), ([300, 40], [420, 40], 0, 0), ([5, 9], [900, 300], 0, 128),
+    ([150, 4], [400, 90], 50, 0), ([7], [700], 100, 128)], ids=str)
+def test_values_of_tokens_a_row_does_not_see(layout, chunks, ctxs, window, part, bad):
+    """V of new tokens that is not finite reaches only the rows that see it, and there only its
+    own channels (so it is for tokens that the window of later rows drops)."""
+    hq, hkv, d, bs, dtype, kind = layout
+    c = chunk_case(len(chunks), hq, hkv, d, bs, dtype, chunks, ctxs, kind, seed=13)
+    clean = c["v"].clone()
+    v = c["v"].clone()
+    # tokens of sequence 0 (positions) and the channels where V is bad
+    n, L = chunks[0], ctxs[0]
+    first = L - n                                      # the first new token's position
+    spots = {L - 1: [0, d - 1], L - 1 - n // 3: [5], first + 1: [33, 34], first: [33]}
+    if window:
+        spots[max(0, first - window + 1)] = [7]        # seen by the first row alone
+    for pos, channels in spots.items():
+        at = int(c["tables"][0, pos // bs]), pos % bs
+        for ch in channels:
+            v[at[0], at[1], :, ch] = 0x7f if kind == "e4m3" else float(bad)
+    g = on_gpu(dict(c, v=v))
+    got = call(g, window=window, partition_tokens=part)
+    place = call(g, window=window, partition_tokens=part, out=g["q"])      # in place
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error() == 0
+    assert torch.equal(got.nan_to_num(), place.nan_to_num())
+    got = got.cpu().double()
+    # what a row sees of the bad spots; zeros in their places for those that see none
+    zero = v.clone()
+    zero[~torch.isfinite(v.view(torch.float8_e4m3fn).double() if kind == "e4m3" else v.double())] = 0
+    for name in ("clean", "zero"):
+        want, bound = attend_chunk(c["q"], c["k"], clean if name == "clean" else zero, c["cu"],
+                                   c["tables"], c["lens"], c["scale"], c["out"], window,
+                                   c["k_scale"], c["v_scale"])
+        for b in range(len(chunks)):
+            for i in range(chunks[b]):
+                r, pos = int(c["cu"][b]) + i, ctxs[b] - chunks[b] + i
+                lo = max(0, pos - window + 1) if window else 0
+                sees = torch.zeros(d, dtype=torch.bool)
+                if b == 0:
+                    for p, channels in spots.items():
+                        if lo <= p <= pos:
+                            sees[channels] = True
+                assert not bool(torch.isfinite(got[r][:, sees]).any()), (b, i)
+                err = (got[r] - want[r]).abs()[:, ~sees]
+                assert bool((err <= bound[r][:, ~sees]).all()), (name, b, i)
