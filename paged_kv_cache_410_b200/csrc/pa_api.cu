@@ -920,11 +920,15 @@ pa_status launch_chunk_m(const pa::ChunkParams& p, const ChunkPlan& pl, cudaStre
   // A batch may mix chunks with sequences that decode a token or a few. With
   // more (sequence, KV head) pairs than one-tile CTAs fit on the GPU, the long
   // chunks go in two-tile CTAs and the others, behind them, in one-tile CTAs
-  // (two per SM), which fill the SMs that the first launch's last CTAs leave:
-  // 128 requests, one in twenty a chunk of 64 to 512, the others one token,
-  // 8 KV heads: 286 -> 241 us (f16), 403 -> 326 us (E4M3). With fewer, one launch
-  // of two-tile CTAs: 32 requests, three in ten a chunk: 135 and 137 us (f16),
-  // 240 against 280 us (E4M3).
+  // (two per SM), which fill the SMs that the first launch's last CTAs leave.
+  // Requests with 16 to 4096 cached tokens that bring one token, but some that
+  // bring 64 to 512, 8 KV heads, f16 / E4M3 cache, one launch -> two:
+  //   128 requests, 5 % chunks, 32 heads   312 -> 281 us, 427 -> 360 us
+  //   128 requests, 20 % chunks, 64 heads  860 -> 764 us, 875 -> 831 us
+  //    48 requests, 10 % chunks, 32 heads  200 -> 170 us, 240 -> 198 us
+  //   200 requests, 2 % chunks, 32 heads   469 -> 432 us, 600 -> 482 us
+  // With fewer, one launch of two-tile CTAs: 32 requests, 30 % chunks: 135 against
+  // 137 us (f16), 240 against 280 us (E4M3).
   if (p.num_partitions > 1 || !chunk_longest_first(p, 1))
     return launch_chunk_t<TQ, D, 2, MODE>(p, tq, tk, tv, st);
   pa::ChunkParams a = p, b = p;

@@ -34,15 +34,17 @@
 // is not finite makes every row of the step NaN; rows that do not see it are
 // found by their result and summed again (chunk_unseen_v).
 //
-// What bounds it, measured on one B200 (1.9 GHz, device time):
+// What bounds it, measured on B200s (perf/operators.py; a GPU's own clock and
+// power make up to a tenth):
 //  - drafts (64 requests, 2 to 8 new tokens, 512 to 4096 cached ones, 64 / 8
-//    heads of 128, bf16): 118 to 141 us on different GPUs for 636 MB, 0.69 to
-//    0.82 of the copy bandwidth.
-//    One-tile CTAs, two per SM; without the loads the launch takes 103 us,
-//    without the softmax 131: the loads and the tail are what is left.
-//  - prompts (2048 tokens over 16384, 64 / 8 heads, bf16): 910 us (1030
-//    under the power cap of a long run), 1.0 to 1.1 PFLOP/s, 0.6 to 0.66 of the
-//    cuBLAS burst. A step of 64 tokens and 256 rows takes about
+//    heads of 128, bf16): 120 to 133 us for 636 MB, 0.73 to 0.81 of the copy
+//    bandwidth.
+//    One-tile CTAs, two per SM; on a GPU that took up to 141, without the loads
+//    the launch took 103 us, without the softmax 131: the loads and the tail are
+//    what is left.
+//  - prompts (2048 tokens over 16384, 64 / 8 heads, bf16): 1000 to 1045 us, 1.0
+//    PFLOP/s, 0.58 to 0.61 of the cuBLAS burst (single launches of a cool GPU reach
+//    915). A step of 64 tokens and 256 rows takes about
 //    1850 clocks. Its MMAs alone take 1300 (a tcgen05.mma of N = 64 runs in 33
 //    (A in TMEM) to 49 clocks, but one warp needs 60 to issue it), its
 //    exponentials 1024; the rest is the chain S -> P -> P.V -> S of a tile
@@ -51,9 +53,9 @@
 //    fall into step and wait together: 1277 us in all), two warps per row
 //    (1526 us), one MMA warp per tile instead of two (1003 us), a quarter of the
 //    exponentials as polynomials on the FMA pipe (976 against 937 us).
-//  - E4M3 (a mixed batch of 32, 32 / 8 heads): 240 us; the same batch from a f16
-//    cache 136: the loader warps' copies in flight and widening set the pace
-//    (twice the loader warps: 248).
+//  - E4M3 (a mixed batch of 32, 32 / 8 heads): 240 to 250 us; the same batch from
+//    a f16 cache 134: the loader warps' copies in flight and widening set the pace
+//    (twice the loader warps: 248 against 241).
 #pragma once
 
 #include "pa_prefix_umma.cuh"
